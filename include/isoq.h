@@ -357,6 +357,52 @@ int isoq_multi_token_attention(const isoq_params* params, const isoq_cache* cach
                                float scale, void* workspace, size_t workspace_bytes,
                                void* stream);
 
+/* =======================================================================================
+ * Sliding-window attention with sinks on the packed cache.
+ *
+ * A query token at position p attends the cached tokens
+ *   t in [max(0, p - window + 1), p]      (its window, itself among them) and
+ *   t in [0, min(n_sinks, p + 1))         (the first tokens of the sequence, the sinks),
+ * each once where the two overlap; everything else is as in isoq_decode_attention
+ * (the token of sequence s at p = seq_lens[s] - 1) and isoq_multi_token_attention (query
+ * token i of n_q at p = seq_lens[s] - n_q + i; p < 0 sees nothing and its rows are zeros):
+ * the same scores, codebook, rotation, arithmetic and GQA mapping, for every format.  A
+ * window of at least the context's length is the whole context.  Positions are those of
+ * the sequence (the ones K was appended at); nothing is renumbered.
+ *
+ * Pages.  The call visits the pages of [0, n_sinks) and those from the first window token
+ * of the first query token on.  The page-table entries between the two runs are never
+ * read, and what a page holds outside the attended tokens never reaches a result (any
+ * codes, any norms, infinities and NaN included): a caller may recycle a page for another
+ * sequence as soon as the window has passed its last token.
+ *
+ * window >= 1, n_sinks >= 0.  max_seq_len: a host upper bound of seq_lens, the one given
+ * to isoq_window_workspace_bytes; a longer seq_lens[s] is clamped to it (and to the page
+ * table) with ISOQ_ST_LEN_RANGE, a negative one is 0.  out: device, the shape of Q, element
+ * type out_dtype (ISOQ_F32, ISOQ_BF16, ISOQ_F16; the result in binary32 is rounded once,
+ * to nearest).  workspace: device, 16-byte aligned, at least
+ * isoq_window_workspace_bytes(...) bytes (n_q = 1 for the decode); contents need not be
+ * initialised; calls that share a workspace must not overlap.
+ * isoq_window_workspace_bytes returns 0 for sizes that the calls refuse.
+ * Errors: ISOQ_E_ARG (also window < 1, n_sinks < 0, an unknown out_dtype), ISOQ_E_DIM,
+ * ISOQ_E_GQA, ISOQ_E_WORKSPACE, ISOQ_E_DEVICE, ISOQ_E_CUDA.
+ * ===================================================================================== */
+size_t isoq_window_workspace_bytes(int n_seqs, int n_q, int n_q_heads, int n_kv_heads, int d,
+                                   int max_seq_len, int window, int n_sinks);
+
+int isoq_decode_attention_window(const isoq_params* params, const isoq_cache* cache,
+                                 const void* Q, int q_dtype, int n_seqs, int n_q_heads,
+                                 const int32_t* seq_lens, int max_seq_len, int window,
+                                 int n_sinks, void* out, int out_dtype, float scale,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+int isoq_multi_token_attention_window(const isoq_params* params, const isoq_cache* cache,
+                                      const void* Q, int q_dtype, int n_seqs, int n_q,
+                                      int n_q_heads, const int32_t* seq_lens, int max_seq_len,
+                                      int window, int n_sinks, void* out, int out_dtype,
+                                      float scale, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
 /* Number of context chunks (splits) the decode uses for these sizes on the current
  * device; >= 1, or a negative error code. */
 int isoq_decode_num_splits(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_seq_len);

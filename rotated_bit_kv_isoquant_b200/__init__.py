@@ -96,6 +96,11 @@ _SIGS = {
     "isoq_decode_state_bytes": (_sz, [_i, _i, _i]),
     "isoq_multi_token_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "isoq_multi_token_attention": (_i, [_p, _cp, _p, _i, _i, _i, _i, _p, _i, _p, _f, _p, _sz, _p]),
+    "isoq_window_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
+    "isoq_decode_attention_window": (_i, [_p, _cp, _p, _i, _i, _i, _p, _i, _i, _i, _p, _i, _f, _p,
+                                          _sz, _p]),
+    "isoq_multi_token_attention_window": (_i, [_p, _cp, _p, _i, _i, _i, _i, _p, _i, _i, _i, _p, _i,
+                                               _f, _p, _sz, _p]),
     "isoq_decode_partial_state": (_i, [_p, _cp, _p, _i, _i, _i, _p, _i, _p, _f, _p, _sz, _p]),
     "isoq_decode_merge_states": (_i, [_p, _p, _i, _i, _i, _p, _p]),
     "isoq_get_status": (_i, [_cp, ctypes.POINTER(ctypes.c_uint32)]),
@@ -117,12 +122,18 @@ def _check(rc: int, where: str):
     return rc
 
 
+_dtype_codes = {}  # torch dtype -> ISOQ_*, filled at the first use
+
+
 def _dtype_code(t) -> int:
-    import torch
-    m = {torch.float32: ISOQ_F32, torch.bfloat16: ISOQ_BF16, torch.float16: ISOQ_F16}
-    if t.dtype not in m:
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float32: ISOQ_F32, torch.bfloat16: ISOQ_BF16,
+                             torch.float16: ISOQ_F16})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 def _dev_ptr(t, name: str, dtype=None):
@@ -363,6 +374,60 @@ def isoq_multi_token_attention(params: Params, cache: PagedCache, Q, seq_lens, m
         _dev_ptr(out, "out", torch.float32), float(scale), _dev_ptr(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
         "isoq_multi_token_attention")
+
+
+def isoq_window_workspace_bytes(n_seqs, n_q, n_q_heads, n_kv_heads, d, max_seq_len, window,
+                                n_sinks) -> int:
+    return int(_lib.isoq_window_workspace_bytes(n_seqs, n_q, n_q_heads, n_kv_heads, d, max_seq_len,
+                                                window, n_sinks))
+
+
+def _check_window(cache, Q, seq_lens, out, workspace):
+    """The tensors of a windowed call agree in shape and live on the cache's device."""
+    if Q.shape != out.shape or Q.shape[-1] != cache.d:
+        raise ValueError(f"Q and out must have the same shape ending in d = {cache.d}")
+    if seq_lens.numel() < Q.shape[0]:
+        raise ValueError("seq_lens must have one entry per sequence")
+    dev = cache.blocks.device
+    if not (Q.device == out.device == seq_lens.device == workspace.device == dev):
+        raise ValueError(f"Q, seq_lens, out and workspace must be on the cache's device {dev}")
+
+
+def isoq_decode_attention_window(params: Params, cache: PagedCache, Q, seq_lens, max_seq_len: int,
+                                 window: int, n_sinks: int, out, scale: float, workspace,
+                                 stream=None) -> None:
+    """One query token per sequence over the last `window` cached tokens and the first
+    `n_sinks`.  Q: CUDA [n_seqs][n_q_heads][d]; out: the same shape, fp32, bf16 or fp16;
+    workspace: CUDA tensor of >= isoq_window_workspace_bytes(n_seqs, 1, ...) bytes."""
+    import torch
+    if Q.dim() != 3:
+        raise ValueError("Q must be [n_seqs][n_q_heads][d]")
+    _check_window(cache, Q, seq_lens, out, workspace)
+    _check(_lib.isoq_decode_attention_window(
+        params.handle, cache._c, _dev_ptr(Q, "Q"), _dtype_code(Q), Q.shape[0], Q.shape[1],
+        _dev_ptr(seq_lens, "seq_lens", torch.int32), max_seq_len, window, n_sinks,
+        _dev_ptr(out, "out"), _dtype_code(out), scale, _dev_ptr(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
+        "isoq_decode_attention_window")
+
+
+def isoq_multi_token_attention_window(params: Params, cache: PagedCache, Q, seq_lens,
+                                      max_seq_len: int, window: int, n_sinks: int, out,
+                                      scale: float, workspace, stream=None) -> None:
+    """A chunk of query tokens per sequence, each over its own last `window` tokens and the
+    first `n_sinks`.  Q: CUDA [n_seqs][n_q][n_q_heads][d] (query i at position
+    seq_len - n_q + i); out: the same shape, fp32, bf16 or fp16; workspace >=
+    isoq_window_workspace_bytes(...) bytes."""
+    import torch
+    if Q.dim() != 4:
+        raise ValueError("Q must be [n_seqs][n_q][n_q_heads][d]")
+    _check_window(cache, Q, seq_lens, out, workspace)
+    _check(_lib.isoq_multi_token_attention_window(
+        params.handle, cache._c, _dev_ptr(Q, "Q"), _dtype_code(Q), Q.shape[0], Q.shape[1],
+        Q.shape[2], _dev_ptr(seq_lens, "seq_lens", torch.int32), max_seq_len, window, n_sinks,
+        _dev_ptr(out, "out"), _dtype_code(out), scale, _dev_ptr(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
+        "isoq_multi_token_attention_window")
 
 
 def isoq_decode_state_bytes(n_seqs, n_q_heads, d) -> int:

@@ -108,18 +108,15 @@ struct SplitPlan {
 // Context chunking for the decode kernel: about ISOQ_DEC_WAVES waves of (chunk, KV head,
 // query-head block, sequence) CTAs at the kernel's resident CTAs per SM, each chunk a whole
 // number of pages and at least min_pages pages when the context allows.
-SplitPlan plan_splits(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_seq_len,
-                      int n_q = 1) {
+SplitPlan plan_pages(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_pages, int n_q) {
   const int group = n_kv_heads > 0 ? n_q_heads / n_kv_heads : 1;
   // the multi-token kernels (64 or 128 rows per CTA, 2 CTAs per SM) when a chunk gives a
   // KV head at least 16 rows; else the per-row kernel (8 rows per CTA)
-  const bool shared_mq = d == 128 && n_q > 1 && (long long)n_q * group >= 16;
+  const bool shared_mq = isoq::shared_page_rows(d, n_q, group);
   const int n_sm = sm_count() * (shared_mq ? 2 : isoq::decode_i8_resident_ctas(d));
-  const int rows_per_cta = shared_mq ? isoq::attention_rows_per_cta(d, n_q, group)
-                                     : isoq::decode_rows_per_block(d, n_q, group);
+  const int rows_per_cta = isoq::rows_per_cta(d, n_q, group);
   // pages per CTA worth a launch: the tensor-memory kernel rotates 128 queries per CTA
   const int min_pages = shared_mq ? (rows_per_cta == 128 ? 16 : 4) : ISOQ_DEC_MIN_PAGES;
-  const int max_pages = max_seq_len > 0 ? (max_seq_len + ISOQ_PAGE_SIZE - 1) / ISOQ_PAGE_SIZE : 1;
   const long long units =
       (long long)n_seqs * n_kv_heads * (((long long)n_q * group + rows_per_cta - 1) / rows_per_cta);
   const long long target = (long long)n_sm * (shared_mq ? ISOQ_MQ_WAVES : ISOQ_DEC_WAVES);
@@ -133,6 +130,36 @@ SplitPlan plan_splits(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_
   if (pps > isoq::kMaxPagesPerSplit) pps = isoq::kMaxPagesPerSplit;
   int n_splits = (max_pages + pps - 1) / pps;
   return SplitPlan{n_splits, pps};
+}
+
+// Pages of a context of at most len tokens (at least one, so that a plan has a chunk).
+int pages_of(int len) {
+  return len > 0 ? (int)(((long long)len + ISOQ_PAGE_SIZE - 1) / ISOQ_PAGE_SIZE) : 1;
+}
+
+SplitPlan plan_splits(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_seq_len,
+                      int n_q = 1) {
+  return plan_pages(n_seqs, n_q_heads, n_kv_heads, d, pages_of(max_seq_len), n_q);
+}
+
+// Most pages that the rows of one CTA can see with a window of W tokens and S sinks: a CTA
+// of R rows spans at most (R + G - 2) / G + 1 query tokens, and n consecutive tokens touch
+// at most (n + 62) / 64 + 1 pages.
+int window_pages(int n_q_heads, int n_kv_heads, int d, int max_seq_len, int n_q, int window,
+                 int n_sinks) {
+  const long long G = n_q_heads / n_kv_heads > 0 ? n_q_heads / n_kv_heads : 1;
+  const long long R = isoq::rows_per_cta(d, n_q, (int)G);
+  const long long span = n_q < (R + G - 2) / G + 1 ? n_q : (R + G - 2) / G + 1;
+  const long long pages = ((long long)n_sinks + ISOQ_PAGE_SIZE - 1) / ISOQ_PAGE_SIZE +
+                          ((long long)window + span - 1 + ISOQ_PAGE_SIZE - 2) / ISOQ_PAGE_SIZE + 1;
+  const int all = pages_of(max_seq_len);
+  return pages < all ? (int)pages : all;
+}
+
+SplitPlan plan_window(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_seq_len, int n_q,
+                      int window, int n_sinks) {
+  return plan_pages(n_seqs, n_q_heads, n_kv_heads, d,
+                    window_pages(n_q_heads, n_kv_heads, d, max_seq_len, n_q, window, n_sinks), n_q);
 }
 
 int check_cache(const isoq_cache* c, const isoq_params* p) {
@@ -453,10 +480,11 @@ bool rows_fit(int n_q, int n_q_heads, int n_kv_heads) {
 
 // Shared by the decode entry points: validation, the split plan, then the split kernel and
 // the combine into either the output rows (out) or merged states (state).
+// window > 0: sliding-window attention with n_sinks sinks, out of type out_dtype.
 int decode_common_impl(const isoq_params* params, const isoq_cache* cache, const void* Q,
                   int q_dtype, int n_seqs, int n_q, int n_q_heads, const int32_t* seq_lens,
-                  int max_seq_len, float* out, float* state, float scale, void* workspace,
-                  size_t workspace_bytes, void* stream) {
+                  int max_seq_len, int window, int n_sinks, void* out, int out_dtype, float* state,
+                  float scale, void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_cache(cache, params);
   if (rc) return rc;
   if (n_seqs < 0 || n_q_heads < 0 || max_seq_len < 0 || !valid_dtype(q_dtype)) return ISOQ_E_ARG;
@@ -468,12 +496,14 @@ int decode_common_impl(const isoq_params* params, const isoq_cache* cache, const
   if (!Q || !seq_lens || !(out || state) || !workspace) return ISOQ_E_ARG;
   if (state && ((uintptr_t)state & 15u) != 0) return ISOQ_E_ARG;
   if (((uintptr_t)workspace & 15u) != 0) return ISOQ_E_WORKSPACE;
-  const size_t need = isoq_multi_token_workspace_bytes(n_seqs, n_q, n_q_heads, cache->n_kv_heads,
-                                                       cache->d, max_seq_len);
+  const SplitPlan plan =
+      window > 0 ? plan_window(n_seqs, n_q_heads, cache->n_kv_heads, cache->d, max_seq_len, n_q,
+                               window, n_sinks)
+                 : plan_splits(n_seqs, n_q_heads, cache->n_kv_heads, cache->d, max_seq_len, n_q);
+  const size_t need = (size_t)n_seqs * n_q * n_q_heads * plan.n_splits *
+                      isoq::partial_stride(cache->d) * sizeof(float);
   if (workspace_bytes < need) return ISOQ_E_WORKSPACE;
   if ((rc = check_device(params))) return rc;
-  const SplitPlan plan =
-      plan_splits(n_seqs, n_q_heads, cache->n_kv_heads, cache->d, max_seq_len, n_q);
   isoq::DecodeArgs a{};
   a.n_q = n_q;
   a.params = params->dev_mat;
@@ -494,6 +524,10 @@ int decode_common_impl(const isoq_params* params, const isoq_cache* cache, const
   a.pages_per_split = plan.pages_per_split;
   a.partials = static_cast<float*>(workspace);
   a.out = out;
+  a.out_dtype = out_dtype;
+  a.window = window;
+  a.n_sinks = n_sinks;
+  a.max_len = max_seq_len;
   a.state = state;
   a.status = cache->status;
   cudaError_t e = isoq::launch_decode(a, (cudaStream_t)stream);
@@ -508,7 +542,8 @@ int decode_run(const isoq_params* params, const isoq_cache* cache, const void* Q
                float* out, float* state, float scale, void* workspace, size_t workspace_bytes,
                void* stream) {
   return decode_common_impl(params, cache, Q, q_dtype, n_seqs, n_q, n_q_heads, seq_lens,
-                            max_seq_len, out, state, scale, workspace, workspace_bytes, stream);
+                            max_seq_len, 0, 0, out, ISOQ_F32, state, scale, workspace,
+                            workspace_bytes, stream);
 }
 }  // namespace isoq
 
@@ -518,7 +553,20 @@ inline int decode_common(const isoq_params* params, const isoq_cache* cache, con
                          int max_seq_len, float* out, float* state, float scale, void* workspace,
                          size_t workspace_bytes, void* stream) {
   return decode_common_impl(params, cache, Q, q_dtype, n_seqs, n_q, n_q_heads, seq_lens,
-                            max_seq_len, out, state, scale, workspace, workspace_bytes, stream);
+                            max_seq_len, 0, 0, out, ISOQ_F32, state, scale, workspace,
+                            workspace_bytes, stream);
+}
+
+// The windowed entry points: the window's own checks, then the shared body.
+int window_common(const isoq_params* params, const isoq_cache* cache, const void* Q, int q_dtype,
+                  int n_seqs, int n_q, int n_q_heads, const int32_t* seq_lens, int max_seq_len,
+                  int window, int n_sinks, void* out, int out_dtype, float scale, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  if (window < 1 || n_sinks < 0 || !valid_dtype(out_dtype)) return ISOQ_E_ARG;
+  if (!out && n_seqs > 0 && n_q_heads > 0) return ISOQ_E_ARG;
+  return decode_common_impl(params, cache, Q, q_dtype, n_seqs, n_q, n_q_heads, seq_lens,
+                            max_seq_len, window, n_sinks, out, out_dtype, nullptr, scale, workspace,
+                            workspace_bytes, stream);
 }
 }  // namespace
 
@@ -547,6 +595,36 @@ int isoq_multi_token_attention(const isoq_params* params, const isoq_cache* cach
                                void* stream) {
   return decode_common(params, cache, Q, q_dtype, n_seqs, n_q, n_q_heads, seq_lens, max_seq_len,
                        out, nullptr, scale, workspace, workspace_bytes, stream);
+}
+
+size_t isoq_window_workspace_bytes(int n_seqs, int n_q, int n_q_heads, int n_kv_heads, int d,
+                                   int max_seq_len, int window, int n_sinks) {
+  if (n_seqs < 0 || n_q < 1 || n_q_heads < 0 || n_kv_heads < 1 || max_seq_len < 0 || window < 1 ||
+      n_sinks < 0)
+    return 0;
+  if (!supported_d(d) || n_q_heads % n_kv_heads) return 0;
+  const int ns = plan_window(n_seqs, n_q_heads, n_kv_heads, d, max_seq_len, n_q, window, n_sinks)
+                     .n_splits;
+  return (size_t)n_seqs * n_q * n_q_heads * ns * isoq::partial_stride(d) * sizeof(float);
+}
+
+int isoq_decode_attention_window(const isoq_params* params, const isoq_cache* cache,
+                                 const void* Q, int q_dtype, int n_seqs, int n_q_heads,
+                                 const int32_t* seq_lens, int max_seq_len, int window,
+                                 int n_sinks, void* out, int out_dtype, float scale,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  return window_common(params, cache, Q, q_dtype, n_seqs, 1, n_q_heads, seq_lens, max_seq_len,
+                       window, n_sinks, out, out_dtype, scale, workspace, workspace_bytes, stream);
+}
+
+int isoq_multi_token_attention_window(const isoq_params* params, const isoq_cache* cache,
+                                      const void* Q, int q_dtype, int n_seqs, int n_q,
+                                      int n_q_heads, const int32_t* seq_lens, int max_seq_len,
+                                      int window, int n_sinks, void* out, int out_dtype,
+                                      float scale, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  return window_common(params, cache, Q, q_dtype, n_seqs, n_q, n_q_heads, seq_lens, max_seq_len,
+                       window, n_sinks, out, out_dtype, scale, workspace, workspace_bytes, stream);
 }
 
 size_t isoq_decode_state_bytes(int n_seqs, int n_q_heads, int d) {

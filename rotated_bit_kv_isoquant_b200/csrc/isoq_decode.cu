@@ -16,6 +16,7 @@
 #include "isoq_check.cuh"
 #include "isoq_common.cuh"
 #include "isoq_internal.h"
+#include "isoq_window.cuh"
 
 namespace isoq {
 
@@ -29,12 +30,13 @@ namespace isoq {
 // one pass with a running maximum; the groups then merge in shared memory and warp 0
 // finishes.  Launched as a programmatic dependent of the split kernel: the rotation
 // parameters are read before griddepcontrol.wait, the partials after it.
-template <int D, bool FINAL>
+// TYPED: the output rows have the element type out_dtype (else fp32).
+template <int D, bool FINAL, bool TYPED>
 __global__ void __launch_bounds__(128)
     decode_combine_kernel(const float* __restrict__ params, int H, int n_q_heads,
                           int rows_per_seq, int n_splits, const float* __restrict__ partials,
-                          size_t sh_stride, size_t part_stride, float* __restrict__ out,
-                          size_t parts_len, uint32_t* status) {
+                          size_t sh_stride, size_t part_stride, void* __restrict__ out,
+                          size_t parts_len, uint32_t* status, int out_dtype) {
   constexpr int E = D / 32;   // dims per lane
   constexpr int NB = E / 4;
   constexpr int PS = D + 4;
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(128)
 
   const float Ls = red_l[0] + red_l[1] + red_l[2] + red_l[3];
   if constexpr (!FINAL) {
-    float* dst = out + ((size_t)s * rows_per_seq + h) * PS;
+    float* dst = static_cast<float*>(out) + ((size_t)s * rows_per_seq + h) * PS;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int dd = lane * E + i;
@@ -139,19 +141,22 @@ __global__ void __launch_bounds__(128)
   for (int k = 0; k < NB; ++k) mat_inv(Mb[k], o + 4 * k, y + 4 * k);
   wht_warp<E>(y, lane);
   const float rs = rsqrtf((float)D);
-  float* dst = out + ((size_t)s * rows_per_seq + h) * D + lane * E;
+  const size_t ob = ((size_t)s * rows_per_seq + h) * D + lane * E;
 #pragma unroll
-  for (int i = 0; i < E; ++i) dst[i] = y[i] * rs;
+  for (int i = 0; i < E; ++i) {
+    if constexpr (TYPED) store_typed(out, ob + i, y[i] * rs, out_dtype);
+    else static_cast<float*>(out)[ob + i] = y[i] * rs;
+  }
 }
 
 // The combine on `stream` as a programmatic dependent launch of the kernel before it (it
 // may start while that kernel drains; it waits in-kernel for its results).
-template <int D, bool FINAL>
+template <int D, bool FINAL, bool TYPED = false>
 static cudaError_t launch_combine(dim3 grid, cudaStream_t stream, bool dependent,
                                   const float* params, int H, int n_q_heads, int rows_per_seq,
                                   int n_splits, const float* partials, size_t sh_stride,
-                                  size_t part_stride, float* out, size_t parts_len,
-                                  uint32_t* status) {
+                                  size_t part_stride, void* out, size_t parts_len,
+                                  uint32_t* status, int out_dtype = ISOQ_F32) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(128);
@@ -162,9 +167,9 @@ static cudaError_t launch_combine(dim3 grid, cudaStream_t stream, bool dependent
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = dependent ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, decode_combine_kernel<D, FINAL>, params, H, n_q_heads,
+  return cudaLaunchKernelEx(&cfg, decode_combine_kernel<D, FINAL, TYPED>, params, H, n_q_heads,
                             rows_per_seq, n_splits, partials, sh_stride, part_stride, out,
-                            parts_len, status);
+                            parts_len, status, out_dtype);
 }
 
 template <int D>
@@ -183,6 +188,10 @@ static cudaError_t launch_dq(const DecodeArgs& a, cudaStream_t stream) {
     e = launch_combine<D, false>(grid, stream, true, a.params, a.n_kv_heads, a.n_q_heads, rows,
                                  a.n_splits, a.partials, a.n_splits * PS, PS, a.state, parts_len,
                                  a.status);
+  else if (a.window > 0)
+    e = launch_combine<D, true, true>(grid, stream, true, a.params, a.n_kv_heads, a.n_q_heads,
+                                      rows, a.n_splits, a.partials, a.n_splits * PS, PS, a.out,
+                                      parts_len, a.status, a.out_dtype);
   else
     e = launch_combine<D, true>(grid, stream, true, a.params, a.n_kv_heads, a.n_q_heads, rows,
                                 a.n_splits, a.partials, a.n_splits * PS, PS, a.out, parts_len,

@@ -49,6 +49,7 @@
 #include "isoq_internal.h"
 #include "isoq_ptx.cuh"
 #include "isoq_vtile.cuh"
+#include "isoq_window.cuh"
 
 namespace isoq {
 using namespace ptx;
@@ -192,14 +193,16 @@ constexpr int i8_min_blocks(int nw) {
 // out (decode with a single chunk only, else null): the CTA holds the whole context of its
 // rows, so it finishes the combine itself -- normalise, inverse rotation -- and writes the
 // output rows [n_seqs][n_q_heads][D] instead of partials.
-template <int D, int NST, int RB, typename TQ, bool MQ, int NW>
+// WIN: sliding-window attention with sinks (isoq_window.cuh): the chunks are runs of the
+// pages that the rows can see, and out has the element type win.out_dtype.
+template <int D, int NST, int RB, typename TQ, bool MQ, int NW, bool WIN>
 __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
     decode_i8_kernel(const float* __restrict__ params, const uint8_t* __restrict__ blocks,
                      const int32_t* __restrict__ page_table, int n_pages, int max_pages, int H,
                      const TQ* __restrict__ Q, int n_q_heads, int n_q,
                      const int32_t* __restrict__ seq_lens, float scale, int pages_per_split,
                      int n_splits, float* __restrict__ partials, uint32_t* status,
-                     float* __restrict__ out, const I8Mul mk) {
+                     void* __restrict__ out, const I8Mul mk, const WinArgs win) {
   using SM = I8Smem<D, NST, RB, NW>;
   constexpr int E = D / 32;           // elements per lane in the warp WHT layout
   constexpr int NB = E / 4;
@@ -236,17 +239,16 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
     return (R / G) * n_q_heads + hk * G + R % G;
   };
 
-  int len = __ldg(seq_lens + s);
-  if (len > max_pages * kPage) {
-    if (tid == 0 && split == 0 && blockIdx.y == 0) set_status(status, ISOQ_ST_LEN_RANGE);
-    len = max_pages * kPage;
-  }
+  const int len = clamp_len<WIN>(__ldg(seq_lens + s), max_pages, win,
+                                 tid == 0 && split == 0 && blockIdx.y == 0, status);
   // causal limits: lim(r) = len - n_q + 1 + i(r), clamped to [0, len]
   const int lim_lo = MQ ? max(0, min(len, len - n_q + 1 + row_token(0))) : len;
   const int lim_hi = MQ ? max(0, min(len, len - n_q + 1 + row_token(nh - 1))) : len;
   const int lim_g = MQ && rg < nh ? max(0, min(len, len - n_q + 1 + row_token(rg))) : lim_hi;
-  const int p_begin = split * pages_per_split;
-  const int p_end = min((lim_hi + kPage - 1) / kPage, p_begin + pages_per_split);
+  const WinPages<WIN> wp(win, lim_lo, lim_hi);
+  const int lo_g = win_lo<WIN>(win, lim_g);
+  const int p_begin = split * pages_per_split;  // slots of the pages to visit
+  const int p_end = min(wp.n_slots, p_begin + pages_per_split);
 
   float* out_base = partials + ((size_t)s * n_q * n_q_heads) * n_splits * PS + (size_t)split * PS;
   // extents of the checked build: partials / Q rows of the launch, the head's parameters
@@ -262,7 +264,9 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
       for (int i = tid; i < nh * D; i += blockDim.x) {
         const int h = i / D, c = i - h * D;
         const size_t o = ((size_t)s * n_q_heads + row_off[h]) * D + c;
-        if (in_bounds(o < out_len, status)) out[o] = 0.f;
+        if (!in_bounds(o < out_len, status)) continue;
+        if constexpr (WIN) store_typed(out, o, 0.f, win.out_dtype);
+        else static_cast<float*>(out)[o] = 0.f;
       }
       return;
     }
@@ -284,10 +288,10 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
   }
   __syncwarp();
   const int* pt_row = page_table + (size_t)s * max_pages;
-  // page k of this warp = p_begin + warp + NW * k
+  // page k of this warp: slot p_begin + warp + NW * k
   const int n_my = (p_end - p_begin - warp + NW - 1) / NW;  // may be <= 0
   auto issue = [&](int k) {  // lane 0 only
-    const int pg = p_begin + warp + NW * k;
+    const int pg = wp.page(p_begin + warp + NW * k);
     const int st = k % NST;
     const int phys = in_bounds(pg < max_pages && st < NST, status) ? __ldg(pt_row + pg) : -1;
     if (phys >= 0 && phys < n_pages && in_bounds(hk < H, status)) {
@@ -415,13 +419,13 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
       break;
     }
     const uint8_t* blk = myring + st * BB;
-    const int pg = p_begin + warp + NW * k;
+    const int pg = wp.page(p_begin + warp + NW * k);
     const int phys = in_bounds(pg < max_pages && st < NST, status) ? __ldg(pt_row + pg) : -1;
     const bool page_ok = phys >= 0 && phys < n_pages;
     const int tok0 = pg * kPage;
 
     // a page whose 64 tokens are all valid takes the tile body without masking
-    const bool full = page_ok && tok0 + kPage <= lim_lo;
+    const bool full = page_ok && tok0 + kPage <= lim_lo && wp.page_full(win, tok0);
     auto tile = [&](const int tb, auto full_c) {
       constexpr bool FULL = decltype(full_c)::value;
       // ---- a7: scores of 4 tiles of 8 tokens; B = K_hat^T of token tb + 8n + g ----------
@@ -517,8 +521,10 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
         if constexpr (!FULL) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const bool vld = page_ok && (tok0 + tk + c) < lim_hi;
-            sv[n][c] = vld && (!MQ || (tok0 + tk + c) < lim_g) ? sv[n][c] : -CUDART_INF_F;
+            const int tok = tok0 + tk + c;
+            const bool vld = page_ok && tok < lim_hi && wp.any_sees(win, tok);
+            sv[n][c] = vld && (!MQ || (tok < lim_g && win_sees<WIN>(win, lo_g, tok)))
+                           ? sv[n][c] : -CUDART_INF_F;
             nv[n][c] = vld ? nv[n][c] : 0.f;
           }
         }
@@ -732,12 +738,15 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
     const size_t ob = ((size_t)s * n_q_heads + row_off[h]) * D + lane * E;
     if (!in_bounds(ob + E <= out_len, status)) continue;
 #pragma unroll
-    for (int i = 0; i < E; ++i) out[ob + i] = y[i] * rs;
+    for (int i = 0; i < E; ++i) {
+      if constexpr (WIN) store_typed(out, ob + i, y[i] * rs, win.out_dtype);
+      else static_cast<float*>(out)[ob + i] = y[i] * rs;
+    }
   }
 }
 
-template <int D, int NST, int RB, typename TQ, bool MQ, int NW>
-cudaError_t launch_i8_t(const DecodeArgs& a, cudaStream_t stream, float* direct_out) {
+template <int D, int NST, int RB, typename TQ, bool MQ, int NW, bool WIN>
+cudaError_t launch_i8_t(const DecodeArgs& a, cudaStream_t stream, void* direct_out) {
   using SM = I8Smem<D, NST, RB, NW>;
   // the dynamic shared-memory opt-in is per function and per device
   static unsigned long long attr_set = 0;
@@ -745,48 +754,51 @@ cudaError_t launch_i8_t(const DecodeArgs& a, cudaStream_t stream, float* direct_
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !((attr_set >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(decode_i8_kernel<D, NST, RB, TQ, MQ, NW>,
+    e = cudaFuncSetAttribute(decode_i8_kernel<D, NST, RB, TQ, MQ, NW, WIN>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
   const int G = a.n_q_heads / a.n_kv_heads;
   dim3 grid(a.n_splits, a.n_kv_heads * ((a.n_q * G + RB - 1) / RB), a.n_seqs);
-  decode_i8_kernel<D, NST, RB, TQ, MQ, NW><<<grid, NW * 32, SM::kBytes, stream>>>(
+  decode_i8_kernel<D, NST, RB, TQ, MQ, NW, WIN><<<grid, NW * 32, SM::kBytes, stream>>>(
       a.params, a.blocks, a.page_table, a.n_pages, a.max_pages, a.n_kv_heads,
       static_cast<const TQ*>(a.Q), a.n_q_heads, a.n_q, a.seq_lens, a.scale, a.pages_per_split,
       a.n_splits, a.partials, a.status, direct_out,
-      I8Mul{0xFFFFFFFFu});
+      I8Mul{0xFFFFFFFFu}, win_args(a));
   return cudaGetLastError();
 }
 
 // Wide CTAs (more warps, one CTA per SM) when the whole grid fits in one CTA per SM: the
 // GPU would otherwise run a small decode with a few warps per SM, each walking its pages
 // one after another.
-template <int D, int NST, int RB, typename TQ, bool MQ>
-cudaError_t launch_i8_w(const DecodeArgs& a, cudaStream_t stream, float* direct_out) {
+template <int D, int NST, int RB, typename TQ, bool MQ, bool WIN>
+cudaError_t launch_i8_w(const DecodeArgs& a, cudaStream_t stream, void* direct_out) {
   constexpr int kWide = D == 128 ? 16 : 8;
   const int G = a.n_q_heads / a.n_kv_heads;
   const long long ctas =
       (long long)a.n_splits * a.n_kv_heads * ((a.n_q * G + RB - 1) / RB) * a.n_seqs;
   if (ctas <= (long long)decode_i8_sms())
-    return launch_i8_t<D, NST, RB, TQ, MQ, kWide>(a, stream, direct_out);
-  return launch_i8_t<D, NST, RB, TQ, MQ, 4>(a, stream, direct_out);
+    return launch_i8_t<D, NST, RB, TQ, MQ, kWide, WIN>(a, stream, direct_out);
+  return launch_i8_t<D, NST, RB, TQ, MQ, 4, WIN>(a, stream, direct_out);
+}
+
+template <int D, int NST, int RB, typename TQ>
+cudaError_t launch_i8_q(const DecodeArgs& a, cudaStream_t stream, void* direct_out) {
+  const bool mq = a.n_q > 1;
+  if (a.window > 0)
+    return mq ? launch_i8_w<D, NST, RB, TQ, true, true>(a, stream, nullptr)
+              : launch_i8_w<D, NST, RB, TQ, false, true>(a, stream, direct_out);
+  return mq ? launch_i8_w<D, NST, RB, TQ, true, false>(a, stream, nullptr)
+            : launch_i8_w<D, NST, RB, TQ, false, false>(a, stream, direct_out);
 }
 
 template <int D, int NST, int RB>
-cudaError_t launch_i8_rb(const DecodeArgs& a, cudaStream_t stream, float* direct_out) {
-  const bool mq = a.n_q > 1;
+cudaError_t launch_i8_rb(const DecodeArgs& a, cudaStream_t stream, void* direct_out) {
   switch (a.q_dtype) {
-    case ISOQ_F32:
-      return mq ? launch_i8_w<D, NST, RB, float, true>(a, stream, nullptr)
-                : launch_i8_w<D, NST, RB, float, false>(a, stream, direct_out);
-    case ISOQ_BF16:
-      return mq ? launch_i8_w<D, NST, RB, __nv_bfloat16, true>(a, stream, nullptr)
-                : launch_i8_w<D, NST, RB, __nv_bfloat16, false>(a, stream, direct_out);
-    case ISOQ_F16:
-      return mq ? launch_i8_w<D, NST, RB, __half, true>(a, stream, nullptr)
-                : launch_i8_w<D, NST, RB, __half, false>(a, stream, direct_out);
+    case ISOQ_F32: return launch_i8_q<D, NST, RB, float>(a, stream, direct_out);
+    case ISOQ_BF16: return launch_i8_q<D, NST, RB, __nv_bfloat16>(a, stream, direct_out);
+    case ISOQ_F16: return launch_i8_q<D, NST, RB, __half>(a, stream, direct_out);
   }
   return cudaErrorInvalidValue;
 }
@@ -809,7 +821,7 @@ cudaError_t launch_decode_split_i8(const DecodeArgs& a, cudaStream_t stream, boo
   if (a.bits != 3) return cudaErrorInvalidValue;
   const bool direct = ISOQ_I8_DIRECT && combined && a.n_splits == 1 && a.n_q == 1 &&
                       a.state == nullptr && a.out != nullptr;
-  float* out = direct ? a.out : nullptr;
+  void* out = direct ? a.out : nullptr;
   const int rb = decode_rows_per_block(a.d, a.n_q, a.n_q_heads / a.n_kv_heads);
   cudaError_t e = cudaErrorInvalidValue;
   if (a.d == 128)
@@ -836,13 +848,13 @@ int decode_i8_resident_ctas(int d) {
     cudaError_t e;
     if (d == 256) {
       using SM = I8Smem<256, ISOQ_I8_NST256, 4, 4>;
-      auto k = decode_i8_kernel<256, ISOQ_I8_NST256, 4, __nv_bfloat16, false, 4>;
+      auto k = decode_i8_kernel<256, ISOQ_I8_NST256, 4, __nv_bfloat16, false, 4, false>;
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes);
       if (e == cudaSuccess)
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, 4 * 32, SM::kBytes);
     } else {
       using SM = I8Smem<128, ISOQ_I8_NST128, 8, 4>;
-      auto k = decode_i8_kernel<128, ISOQ_I8_NST128, 8, __nv_bfloat16, false, 4>;
+      auto k = decode_i8_kernel<128, ISOQ_I8_NST128, 8, __nv_bfloat16, false, 4, false>;
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes);
       if (e == cudaSuccess)
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, 4 * 32, SM::kBytes);

@@ -34,6 +34,7 @@
 #include "isoq_common.cuh"
 #include "isoq_internal.h"
 #include "isoq_ptx.cuh"
+#include "isoq_window.cuh"
 
 namespace isoq {
 using namespace ptx;
@@ -62,13 +63,15 @@ constexpr int dec_min_blocks() { return D == 128 ? 4 : 2; }
 
 // MQ: chunks of several query tokens per sequence with causal limits; the decode (one
 // query token, every row attending the whole context) is compiled without them.
-template <int D, int NST, typename TQ, bool MQ, int BITS>
+// WIN: sliding-window attention with sinks (isoq_window.cuh).
+template <int D, int NST, typename TQ, bool MQ, int BITS, bool WIN>
 __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
     decode_mma_kernel(const float* __restrict__ params, const uint8_t* __restrict__ blocks,
                       const int32_t* __restrict__ page_table, int n_pages, int max_pages, int H,
                       const TQ* __restrict__ Q, int n_q_heads, int n_q,
                       const int32_t* __restrict__ seq_lens, float scale, int pages_per_split,
-                      int n_splits, float* __restrict__ partials, uint32_t* status) {
+                      int n_splits, float* __restrict__ partials, uint32_t* status,
+                      const WinArgs win) {
   using SM = MmaSmem<D, NST, BITS>;
   constexpr int E = D / 32;           // elements per lane in the warp WHT layout
   constexpr int NB = E / 4;
@@ -103,18 +106,17 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
     return (R / G) * n_q_heads + hk * G + R % G;
   };
 
-  int len = __ldg(seq_lens + s);
-  if (len > max_pages * kPage) {
-    if (tid == 0 && split == 0 && blockIdx.y == 0) set_status(status, ISOQ_ST_LEN_RANGE);
-    len = max_pages * kPage;
-  }
+  const int len = clamp_len<WIN>(__ldg(seq_lens + s), max_pages, win,
+                                 tid == 0 && split == 0 && blockIdx.y == 0, status);
   // causal limits: lim(r) = len - n_q + 1 + i(r), clamped to [0, len]
   const int lim_lo = MQ ? max(0, min(len, len - n_q + 1 + row_token(0))) : len;
   const int lim_hi = MQ ? max(0, min(len, len - n_q + 1 + row_token(nh - 1))) : len;
   const int lim_g =
       MQ && g < nh ? max(0, min(len, len - n_q + 1 + row_token(g))) : lim_hi;
-  const int p_begin = split * pages_per_split;
-  const int p_end = min((lim_hi + kPage - 1) / kPage, p_begin + pages_per_split);
+  const WinPages<WIN> wp(win, lim_lo, lim_hi);
+  const int lo_g = win_lo<WIN>(win, lim_g);
+  const int p_begin = split * pages_per_split;  // slots of the pages to visit
+  const int p_end = min(wp.n_slots, p_begin + pages_per_split);
 
   float* out_base = partials + ((size_t)s * n_q * n_q_heads) * n_splits * PS + (size_t)split * PS;
   // extents of the checked build: partials / Q rows of the launch
@@ -141,10 +143,10 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
   }
   __syncwarp();
   const int* pt_row = page_table + (size_t)s * max_pages;
-  // page k of this warp = p_begin + warp + kWarps * k
+  // page k of this warp: slot p_begin + warp + kWarps * k
   const int n_my = (p_end - p_begin - warp + kWarps - 1) / kWarps;  // may be <= 0
   auto issue = [&](int k) {  // lane 0 only
-    const int pg = p_begin + warp + kWarps * k;
+    const int pg = wp.page(p_begin + warp + kWarps * k);
     const int st = k % NST;
     const int phys = in_bounds(pg < max_pages && st < NST, status) ? __ldg(pt_row + pg) : -1;
     if (phys >= 0 && phys < n_pages && in_bounds(hk < H, status)) {
@@ -231,13 +233,13 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
       break;
     }
     const uint8_t* blk = myring + st * BB;
-    const int pg = p_begin + warp + kWarps * k;
+    const int pg = wp.page(p_begin + warp + kWarps * k);
     const int phys = in_bounds(pg < max_pages && st < NST, status) ? __ldg(pt_row + pg) : -1;
     const bool page_ok = phys >= 0 && phys < n_pages;
     const int tok0 = pg * kPage;
 
     // a page whose 64 tokens are all valid takes the tile body without masking
-    const bool full = page_ok && tok0 + kPage <= lim_lo;
+    const bool full = page_ok && tok0 + kPage <= lim_lo && wp.page_full(win, tok0);
     auto tile = [&](const int tb, auto full_c) {
       constexpr bool FULL = decltype(full_c)::value;
       // ---- a7: scores of 4 tiles of 8 tokens; B = K_hat^T of token tb + 8n + g ------------
@@ -289,10 +291,13 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
         nv[n][0] = nv2.x;
         nv[n][1] = nv2.y;
         if constexpr (!FULL) {
-          const bool v0 = page_ok && (tok0 + tk) < lim_hi;
-          const bool v1 = page_ok && (tok0 + tk + 1) < lim_hi;
-          sv[n][0] = v0 && (!MQ || (tok0 + tk) < lim_g) ? sv[n][0] : -CUDART_INF_F;
-          sv[n][1] = v1 && (!MQ || (tok0 + tk + 1) < lim_g) ? sv[n][1] : -CUDART_INF_F;
+          const int tok = tok0 + tk;
+          const bool v0 = page_ok && tok < lim_hi && wp.any_sees(win, tok);
+          const bool v1 = page_ok && tok + 1 < lim_hi && wp.any_sees(win, tok + 1);
+          sv[n][0] = v0 && (!MQ || (tok < lim_g && win_sees<WIN>(win, lo_g, tok)))
+                         ? sv[n][0] : -CUDART_INF_F;
+          sv[n][1] = v1 && (!MQ || (tok + 1 < lim_g && win_sees<WIN>(win, lo_g, tok + 1)))
+                         ? sv[n][1] : -CUDART_INF_F;
           nv[n][0] = v0 ? nv[n][0] : 0.f;
           nv[n][1] = v1 ? nv[n][1] : 0.f;
         }
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
   }
 }
 
-template <int D, int NST, typename TQ, bool MQ, int BITS>
+template <int D, int NST, typename TQ, bool MQ, int BITS, bool WIN>
 static cudaError_t launch_mma_t(const DecodeArgs& a, cudaStream_t stream) {
   using SM = MmaSmem<D, NST, BITS>;
   // the dynamic shared-memory opt-in is per function and per device
@@ -484,33 +489,36 @@ static cudaError_t launch_mma_t(const DecodeArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !((attr_set >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(decode_mma_kernel<D, NST, TQ, MQ, BITS>,
+    e = cudaFuncSetAttribute(decode_mma_kernel<D, NST, TQ, MQ, BITS, WIN>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
   const int G = a.n_q_heads / a.n_kv_heads;
   dim3 grid(a.n_splits, a.n_kv_heads * ((a.n_q * G + 7) / 8), a.n_seqs);
-  decode_mma_kernel<D, NST, TQ, MQ, BITS><<<grid, kWarps * 32, SM::kBytes, stream>>>(
+  decode_mma_kernel<D, NST, TQ, MQ, BITS, WIN><<<grid, kWarps * 32, SM::kBytes, stream>>>(
       a.params, a.blocks, a.page_table, a.n_pages, a.max_pages, a.n_kv_heads,
       static_cast<const TQ*>(a.Q), a.n_q_heads, a.n_q, a.seq_lens, a.scale, a.pages_per_split,
-      a.n_splits, a.partials, a.status);
+      a.n_splits, a.partials, a.status, win_args(a));
   return cudaGetLastError();
+}
+
+template <int D, int NST, int BITS, typename TQ>
+static cudaError_t launch_mma_q(const DecodeArgs& a, cudaStream_t stream) {
+  const bool mq = a.n_q > 1;
+  if (a.window > 0)
+    return mq ? launch_mma_t<D, NST, TQ, true, BITS, true>(a, stream)
+              : launch_mma_t<D, NST, TQ, false, BITS, true>(a, stream);
+  return mq ? launch_mma_t<D, NST, TQ, true, BITS, false>(a, stream)
+            : launch_mma_t<D, NST, TQ, false, BITS, false>(a, stream);
 }
 
 template <int D, int NST, int BITS>
 cudaError_t launch_decode_mma_b(const DecodeArgs& a, cudaStream_t stream) {
-  const bool mq = a.n_q > 1;
   switch (a.q_dtype) {
-    case ISOQ_F32:
-      return mq ? launch_mma_t<D, NST, float, true, BITS>(a, stream)
-                : launch_mma_t<D, NST, float, false, BITS>(a, stream);
-    case ISOQ_BF16:
-      return mq ? launch_mma_t<D, NST, __nv_bfloat16, true, BITS>(a, stream)
-                : launch_mma_t<D, NST, __nv_bfloat16, false, BITS>(a, stream);
-    case ISOQ_F16:
-      return mq ? launch_mma_t<D, NST, __half, true, BITS>(a, stream)
-                : launch_mma_t<D, NST, __half, false, BITS>(a, stream);
+    case ISOQ_F32: return launch_mma_q<D, NST, BITS, float>(a, stream);
+    case ISOQ_BF16: return launch_mma_q<D, NST, BITS, __nv_bfloat16>(a, stream);
+    case ISOQ_F16: return launch_mma_q<D, NST, BITS, __half>(a, stream);
   }
   return cudaErrorInvalidValue;
 }
@@ -556,11 +564,11 @@ int decode_resident_ctas(int d) {
       e = cudaSuccess;
     } else {
       using SM = MmaSmem<128, ISOQ_DEC_NST128, 4>;
-      e = cudaFuncSetAttribute(decode_mma_kernel<128, ISOQ_DEC_NST128, __nv_bfloat16, false, 4>,
+      e = cudaFuncSetAttribute(decode_mma_kernel<128, ISOQ_DEC_NST128, __nv_bfloat16, false, 4, false>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes);
       if (e == cudaSuccess)
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-            &n, decode_mma_kernel<128, ISOQ_DEC_NST128, __nv_bfloat16, false, 4>, kWarps * 32, SM::kBytes);
+            &n, decode_mma_kernel<128, ISOQ_DEC_NST128, __nv_bfloat16, false, 4, false>, kWarps * 32, SM::kBytes);
     }
     if (e != cudaSuccess || n < 1) {
       cudaGetLastError();

@@ -31,6 +31,7 @@
 #include "isoq_common.cuh"
 #include "isoq_internal.h"
 #include "isoq_ptx.cuh"
+#include "isoq_window.cuh"
 #include "isoq_vtile.cuh"
 #include "isoq_tc.cuh"
 
@@ -72,13 +73,15 @@ __device__ __forceinline__ void st_v4(uint32_t addr, const uint32_t (&o)[4]) {
                : "memory");
 }
 
-template <typename TQ, int BITS>
+// WIN: sliding-window attention with sinks (isoq_window.cuh).
+template <typename TQ, int BITS, bool WIN>
 __global__ void __launch_bounds__(kXRows, 2)
     decode_mqtc_kernel(const float* __restrict__ params, const uint8_t* __restrict__ blocks,
                        const int32_t* __restrict__ page_table, int n_pages, int max_pages,
                        int H, const TQ* __restrict__ Q, int n_q_heads, int n_q,
                        const int32_t* __restrict__ seq_lens, float scale, int pages_per_split,
-                       int n_splits, float* __restrict__ partials, uint32_t* status) {
+                       int n_splits, float* __restrict__ partials, uint32_t* status,
+                     const WinArgs win) {
   using SM = MqtcSmem<BITS>;
   constexpr int D = kXD, E = D / 32, NB = E / 4, PS = D + 4;
   constexpr int CB = code_bytes(D, BITS), BB = block_bytes(D, BITS), W = BITS;
@@ -105,11 +108,8 @@ __global__ void __launch_bounds__(kXRows, 2)
   const int row0 = rg * kXRows;
   const int nh = min(kXRows, n_rows - row0);  // rows handled here
 
-  int len = __ldg(seq_lens + s);
-  if (len > max_pages * kPage) {
-    if (tid == 0 && split == 0 && blockIdx.y == 0) set_status(status, ISOQ_ST_LEN_RANGE);
-    len = max_pages * kPage;
-  }
+  const int len = clamp_len<WIN>(__ldg(seq_lens + s), max_pages, win,
+                                 tid == 0 && split == 0 && blockIdx.y == 0, status);
   // row r = pair R = row0 + r: query token R / G, head hk * G + R % G, which sits at
   // position len - n_q + R / G and attends the tokens before and at it
   {
@@ -119,8 +119,11 @@ __global__ void __launch_bounds__(kXRows, 2)
   auto lim_of = [&](int r) { return max(0, min(len, len - n_q + 1 + (row0 + r) / G)); };
   const int lim_hi = lim_of(nh - 1), lim_lo = lim_of(0);
   const int my_lim = tid < nh ? lim_of(tid) : lim_hi;
-  const int p_begin = split * pages_per_split;
-  const int p_end = min((lim_hi + kPage - 1) / kPage, p_begin + pages_per_split);
+  const int my_lo = win_lo<WIN>(win, my_lim);
+  auto sees = [&](int tok) { return tok < my_lim && win_sees<WIN>(win, my_lo, tok); };
+  const WinPages<WIN> wp(win, lim_lo, lim_hi);
+  const int p_begin = split * pages_per_split;  // slots of the pages to visit
+  const int p_end = min(wp.n_slots, p_begin + pages_per_split);
   float* out_base = partials + ((size_t)s * n_q * n_q_heads) * n_splits * PS + (size_t)split * PS;
   __syncthreads();
   if (p_begin >= p_end) {  // empty chunk: m = -inf, l = 0, acc = 0
@@ -138,7 +141,8 @@ __global__ void __launch_bounds__(kXRows, 2)
   if (warp == 0) tc::alloc(tmem_slot, kXCols);
   auto issue = [&](int k) {  // thread 0
     const int st = k & 1;
-    const int phys = in_bounds(p_begin + k < max_pages, status) ? __ldg(pt_row + p_begin + k) : -1;
+    const int pg = wp.page(p_begin + k);
+    const int phys = in_bounds(pg < max_pages, status) ? __ldg(pt_row + pg) : -1;
     if (phys >= 0 && phys < n_pages) {
       mbar_expect_tx(bars + st, BB);
       bulk_copy(smem + SM::kOffRing + st * BB, blocks + ((size_t)phys * H + hk) * BB, BB, bars + st);
@@ -270,11 +274,14 @@ __global__ void __launch_bounds__(kXRows, 2)
   // Per page k: K_hat(k) -> tile; S(k) issued; V_hat(k) -> tile while S(k) runs; softmax;
   // O += P' V_hat issued, which runs while the next page's K_hat is dequantised.
   // page-table entry of the next page, loaded one page ahead (off the per-page chain)
-  int phys_nx = n_my > 0 && in_bounds(p_begin < max_pages, status) ? __ldg(pt_row + p_begin) : -1;
+  auto phys_of = [&](int kk) {
+    const int pg = wp.page(p_begin + kk);
+    return in_bounds(pg < max_pages, status) ? __ldg(pt_row + pg) : -1;
+  };
+  int phys_nx = n_my > 0 ? phys_of(0) : -1;
   for (; k < n_my; ++k) {
     const int phys = phys_nx;
-    if (k + 1 < n_my)
-      phys_nx = in_bounds(p_begin + k + 1 < max_pages, status) ? __ldg(pt_row + p_begin + k + 1) : -1;
+    if (k + 1 < n_my) phys_nx = phys_of(k + 1);
     // Three CTA barriers per page; every other hand-off is a thread's own mbarrier wait.
     // The K tile is free: S(k-1) completed before this thread's softmax read it.
     bool ok = mbar_wait(bars + (k & 1), (k >> 1) & 1);
@@ -301,10 +308,10 @@ __global__ void __launch_bounds__(kXRows, 2)
     // thread's own wait); the norms of page k-1 were read before the last barrier
     ok = k == 0 || mbar_wait(bar_pv, (k - 1) & 1);
     if (ok) dequant(k & 1, 1);
-    const int pg = p_begin + k;
+    const int pg = wp.page(p_begin + k);
     const bool page_ok = phys >= 0 && phys < n_pages;
     const int tok0 = pg * kPage;
-    const bool full = page_ok && tok0 + kPage <= lim_lo;
+    const bool full = page_ok && tok0 + kPage <= lim_lo && wp.page_full(win, tok0);
     // norms: nrm[j] = |k_j| kf; nrm[64 + j] = |v_j| / sigma', where sigma' is the CTA's
     // V-norm reference (shared by all rows: it only scales the weights), raised when a
     // token valid for some row has |v| > kSigmaSlack sigma; computed by warps 2 and 3
@@ -315,7 +322,7 @@ __global__ void __launch_bounds__(kXRows, 2)
       } else {
         const int j = tid - 64;
         float nv = half_at(blk + v_norm_off(D, BITS) + 2 * j);
-        nv = page_ok && tok0 + j < lim_hi ? nv : 0.f;
+        nv = page_ok && tok0 + j < lim_hi && wp.any_sees(win, tok0 + j) ? nv : 0.f;
         float pm = nv;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, o));
@@ -366,7 +373,7 @@ __global__ void __launch_bounds__(kXRows, 2)
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
           float sc = x[j] * nrm[j];
-          if constexpr (!FULL) sc = page_ok && tok0 + j < my_lim ? sc : -CUDART_INF_F;
+          if constexpr (!FULL) sc = page_ok && sees(tok0 + j) ? sc : -CUDART_INF_F;
           x[j] = sc;
           tm[j & 3] = fmaxf(tm[j & 3], sc);
         }
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(kXRows, 2)
           for (int e = 0; e < 4; ++e) {
             const int j = j4 + e;
             float a = av[e];
-            if constexpr (!FULL) a = page_ok && tok0 + j < my_lim ? a : -CUDART_INF_F;
+            if constexpr (!FULL) a = page_ok && sees(tok0 + j) ? a : -CUDART_INF_F;
             x[j] = a;
             am[e] = fmaxf(am[e], a);
           }
@@ -511,7 +518,7 @@ __global__ void __launch_bounds__(kXRows, 2)
   }
 }
 
-template <typename TQ, int BITS>
+template <typename TQ, int BITS, bool WIN>
 cudaError_t launch_mqtc_t(const DecodeArgs& a, cudaStream_t stream) {
   using SM = MqtcSmem<BITS>;
   static unsigned long long attr_set = 0;
@@ -519,26 +526,32 @@ cudaError_t launch_mqtc_t(const DecodeArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !((attr_set >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(decode_mqtc_kernel<TQ, BITS>,
+    e = cudaFuncSetAttribute(decode_mqtc_kernel<TQ, BITS, WIN>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
   const int G = a.n_q_heads / a.n_kv_heads;
   dim3 grid(a.n_splits, a.n_kv_heads * ((a.n_q * G + kXRows - 1) / kXRows), a.n_seqs);
-  decode_mqtc_kernel<TQ, BITS><<<grid, kXRows, SM::kBytes, stream>>>(
+  decode_mqtc_kernel<TQ, BITS, WIN><<<grid, kXRows, SM::kBytes, stream>>>(
       a.params, a.blocks, a.page_table, a.n_pages, a.max_pages, a.n_kv_heads,
       static_cast<const TQ*>(a.Q), a.n_q_heads, a.n_q, a.seq_lens, a.scale, a.pages_per_split,
-      a.n_splits, a.partials, a.status);
+      a.n_splits, a.partials, a.status, win_args(a));
   return cudaGetLastError();
+}
+
+template <typename TQ, int BITS>
+cudaError_t launch_mqtc_q(const DecodeArgs& a, cudaStream_t stream) {
+  return a.window > 0 ? launch_mqtc_t<TQ, BITS, true>(a, stream)
+                      : launch_mqtc_t<TQ, BITS, false>(a, stream);
 }
 
 template <int BITS>
 cudaError_t launch_mqtc_b(const DecodeArgs& a, cudaStream_t stream) {
   switch (a.q_dtype) {
-    case ISOQ_F32: return launch_mqtc_t<float, BITS>(a, stream);
-    case ISOQ_BF16: return launch_mqtc_t<__nv_bfloat16, BITS>(a, stream);
-    case ISOQ_F16: return launch_mqtc_t<__half, BITS>(a, stream);
+    case ISOQ_F32: return launch_mqtc_q<float, BITS>(a, stream);
+    case ISOQ_BF16: return launch_mqtc_q<__nv_bfloat16, BITS>(a, stream);
+    case ISOQ_F16: return launch_mqtc_q<__half, BITS>(a, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -56,7 +56,11 @@ struct DecodeArgs {
   int n_splits;         // context chunks per (sequence, KV head)
   int pages_per_split;  // pages in each chunk
   float* partials;      // [n_seqs][n_q][n_q_heads][n_splits][d + 4]
-  float* out;           // [n_seqs][n_q][n_q_heads][d] (when state is null)
+  void* out;            // [n_seqs][n_q][n_q_heads][d] (when state is null), out_dtype
+  int out_dtype;        // ISOQ_F32 unless a window is set
+  int window;           // > 0: sliding-window attention over the last `window` tokens ...
+  int n_sinks;          // ... and the first n_sinks; 0: the whole context
+  int max_len;          // the bound of the lengths that the split plan was made for
   float* state;         // if set: merged state [n_seqs][n_q][n_q_heads][d + 4] instead of out
   uint32_t* status;
 };
@@ -107,6 +111,16 @@ inline int attention_rows_per_cta(int d, int n_q, int group) {
   const long long rows = (long long)n_q * group;
   if (d != 128 || n_q <= 1 || rows < 16) return 8;
   return rows >= ISOQ_MQTC_MIN_ROWS ? 128 : 64;
+}
+
+// A chunk of query tokens that takes the kernels in which 64 or 128 rows share a page.
+inline bool shared_page_rows(int d, int n_q, int group) {
+  return d == 128 && n_q > 1 && (long long)n_q * group >= 16;
+}
+// Rows per CTA of the attention kernel that a call takes.
+inline int rows_per_cta(int d, int n_q, int group) {
+  return shared_page_rows(d, n_q, group) ? attention_rows_per_cta(d, n_q, group)
+                                         : decode_rows_per_block(d, n_q, group);
 }
 
 // Accessors of the opaque parameter handle (defined in isoq_api.cu).
