@@ -258,6 +258,42 @@ int isoq_quantize_append_layers(const isoq_params* const* params,
                                 const float* rope_table, int rope_max_pos, void* stream);
 
 /* =======================================================================================
+ * Read-back.
+ *
+ * For every listed token t < n_tokens and KV head h, the cached vectors as the cache
+ * represents them: K[t][h] = (n / sqrt d) R_h^T L[c] with the codes c and the binary16
+ * norm n of slot positions[t] % 64 of page page_table[seq_ids[t]][positions[t] / 64], R_h
+ * the KV head's rotation; V[t][h] likewise.  No renormalisation, and nothing of the
+ * quantisation error is undone.  The inverse of isoq_quantize_append, for a consumer of
+ * full-precision vectors (a prefix handed to another path, another format of the cache,
+ * keys moved to other positions).
+ *
+ * isoq_dequantize_rope: with the rotary position embedding of K taken off: dims
+ *   (i, i + d/2) are rotated by minus the angle with (cos, sin) = rope_table[position][i],
+ *   the inverse of what isoq_quantize_append_rope applies with the same table.  V as
+ *   isoq_dequantize.
+ *
+ * K, V: device [n_tokens][n_kv_heads][d] contiguous, 16-byte aligned, element type `dtype`
+ * (ISOQ_F32, ISOQ_BF16 or ISOQ_F16; rounded once, to nearest); either may be NULL and is
+ * then not read, not both.  seq_ids, positions: device int32 [n_tokens], in any order, any
+ * token any number of times.  A token whose sequence, position (with a rope_table:
+ * position >= rope_max_pos too) or page is out of range is skipped with
+ * ISOQ_ST_SEQ_RANGE / _POS_RANGE / _PAGE_RANGE: its rows of K and V stay as they were.  A
+ * slot that was never appended reads as whatever its bytes stand for.  rope_table: device,
+ * 16-byte aligned, as for isoq_quantize_append_rope.  n_tokens == 0 is a no-op.
+ * Arithmetic: the levels and the rotation in binary32.
+ * Errors: ISOQ_E_ARG, ISOQ_E_DIM, ISOQ_E_DEVICE, ISOQ_E_CUDA.
+ * ===================================================================================== */
+int isoq_dequantize(const isoq_params* params, const isoq_cache* cache, const int32_t* seq_ids,
+                    const int32_t* positions, int n_tokens, void* K, void* V, int dtype,
+                    void* stream);
+
+int isoq_dequantize_rope(const isoq_params* params, const isoq_cache* cache,
+                         const int32_t* seq_ids, const int32_t* positions, int n_tokens, void* K,
+                         void* V, int dtype, const float* rope_table, int rope_max_pos,
+                         void* stream);
+
+/* =======================================================================================
  * Decode attention on the packed cache (one query token per sequence).
  *
  * For sequence s and query head h (KV head g = h / (n_q_heads / n_kv_heads)):

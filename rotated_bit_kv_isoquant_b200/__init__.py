@@ -96,6 +96,8 @@ _SIGS = {
     "isoq_decode_state_bytes": (_sz, [_i, _i, _i]),
     "isoq_multi_token_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "isoq_multi_token_attention": (_i, [_p, _cp, _p, _i, _i, _i, _i, _p, _i, _p, _f, _p, _sz, _p]),
+    "isoq_dequantize": (_i, [_p, _cp, _p, _p, _i, _p, _p, _i, _p]),
+    "isoq_dequantize_rope": (_i, [_p, _cp, _p, _p, _i, _p, _p, _i, _p, _i, _p]),
     "isoq_window_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
     "isoq_decode_attention_window": (_i, [_p, _cp, _p, _i, _i, _i, _p, _i, _i, _i, _p, _i, _f, _p,
                                           _sz, _p]),
@@ -318,6 +320,51 @@ def isoq_quantize_append_layers(params_list, caches, Ks, Vs, seq_ids, positions,
         _dev_ptr(rope_table, "rope_table", torch.float32) if rope_table is not None else None,
         rope_table.shape[0] if rope_table is not None else 0, _stream_ptr(stream)),
         "isoq_quantize_append_layers")
+
+
+def _check_read(cache, seq_ids, positions, K, V):
+    """The tensors of a read-back agree in shape and type and live on the cache's device;
+    returns the output (K, or V where K is None) that gives the element type."""
+    first = V if K is None else K
+    if first is None:
+        raise ValueError("K or V must be given")
+    n, dev = seq_ids.numel(), cache.blocks.device
+    if seq_ids.dim() != 1 or positions.shape != seq_ids.shape:
+        raise ValueError("seq_ids and positions must be of one length")
+    for x in (K, V):
+        if x is not None and (x.shape != (n, cache.n_kv_heads, cache.d) or x.dtype != first.dtype):
+            raise ValueError(f"K and V must be [{n}][{cache.n_kv_heads}][{cache.d}] of one dtype")
+    if any(x is not None and x.device != dev for x in (seq_ids, positions, K, V)):
+        raise ValueError(f"seq_ids, positions, K and V must be on the cache's device {dev}")
+    return first
+
+
+def isoq_dequantize(params: Params, cache: PagedCache, seq_ids, positions, K=None, V=None,
+                    stream=None) -> None:
+    """The cached vectors of tokens (seq_ids[t], positions[t]) into K and V: CUDA
+    [n_tokens][n_kv_heads][d], fp32, bf16 or fp16; either may be None."""
+    import torch
+    first = _check_read(cache, seq_ids, positions, K, V)
+    _check(_lib.isoq_dequantize(
+        params.handle, cache._c, _dev_ptr(seq_ids, "seq_ids", torch.int32),
+        _dev_ptr(positions, "positions", torch.int32), seq_ids.shape[0], _dev_ptr(K, "K"),
+        _dev_ptr(V, "V"), _dtype_code(first), _stream_ptr(stream)), "isoq_dequantize")
+
+
+def isoq_dequantize_rope(params: Params, cache: PagedCache, seq_ids, positions, K, V, rope_table,
+                         stream=None) -> None:
+    """isoq_dequantize with the rotary embedding taken off K: the inverse of
+    isoq_quantize_append_rope with the same rope_table (isoq_rope_table)."""
+    import torch
+    first = _check_read(cache, seq_ids, positions, K, V)
+    if rope_table.dim() != 3 or rope_table.shape[1:] != (cache.d // 2, 2) or \
+            rope_table.device != cache.blocks.device:
+        raise ValueError(f"rope_table must be [max_pos][{cache.d // 2}][2] on the cache's device")
+    _check(_lib.isoq_dequantize_rope(
+        params.handle, cache._c, _dev_ptr(seq_ids, "seq_ids", torch.int32),
+        _dev_ptr(positions, "positions", torch.int32), seq_ids.shape[0], _dev_ptr(K, "K"),
+        _dev_ptr(V, "V"), _dtype_code(first), _dev_ptr(rope_table, "rope_table", torch.float32),
+        rope_table.shape[0], _stream_ptr(stream)), "isoq_dequantize_rope")
 
 
 def isoq_decode_workspace_bytes(n_seqs, n_q_heads, n_kv_heads, d, max_seq_len) -> int:

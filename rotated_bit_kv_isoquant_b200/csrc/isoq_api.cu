@@ -394,6 +394,43 @@ int quantize_common(const isoq_params* const* params, const isoq_cache* const* c
   return ISOQ_OK;
 }
 
+// Shared by the read-back entry points.
+int dequantize_common(const isoq_params* params, const isoq_cache* cache, const int32_t* seq_ids,
+                      const int32_t* positions, int n_tokens, void* K, void* V, int dtype,
+                      const float* rope, int rope_max_pos, void* stream) {
+  int rc = check_cache(cache, params);
+  if (rc) return rc;
+  if (n_tokens < 0 || !valid_dtype(dtype)) return ISOQ_E_ARG;
+  if (cache->n_kv_heads > 65535) return ISOQ_E_ARG;  // heads are a grid dimension
+  if (n_tokens == 0) return ISOQ_OK;
+  if (!seq_ids || !positions || (!K && !V)) return ISOQ_E_ARG;
+  // the kernels write whole vectors in 16-byte pieces
+  if (((uintptr_t)K & 15u) != 0 || ((uintptr_t)V & 15u) != 0 || ((uintptr_t)rope & 15u) != 0)
+    return ISOQ_E_ARG;
+  if ((rc = check_device(params))) return rc;
+  isoq::DequantizeArgs a{};
+  a.mats = params->dev_mat;
+  a.bits = params->bits;
+  a.n_kv_heads = cache->n_kv_heads;
+  a.d = cache->d;
+  a.blocks = cache->blocks;
+  a.page_table = cache->page_table;
+  a.n_pages = cache->n_pages;
+  a.max_pages = cache->max_pages_per_seq;
+  a.n_seqs = cache->n_seqs;
+  a.status = cache->status;
+  a.seq_ids = seq_ids;
+  a.positions = positions;
+  a.n_tokens = n_tokens;
+  a.K = K;
+  a.V = V;
+  a.dtype = dtype;
+  a.rope = rope;
+  a.rope_max_pos = rope_max_pos;
+  cudaError_t e = isoq::launch_dequantize(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? ISOQ_OK : cuda_fail(e);
+}
+
 // Device fp64 cos/sin table of the rotary embedding.
 __global__ void rope_table_kernel(float* dst, int d, int max_pos, double base) {
   const int h = d / 2;
@@ -436,6 +473,22 @@ int isoq_quantize_append_layers(const isoq_params* const* params,
                                 const float* rope_table, int rope_max_pos, void* stream) {
   return quantize_common(params, caches, K, V, n_layers, dtype, n_tokens, seq_ids, positions,
                          rope_table, rope_max_pos, stream);
+}
+
+int isoq_dequantize(const isoq_params* params, const isoq_cache* cache, const int32_t* seq_ids,
+                    const int32_t* positions, int n_tokens, void* K, void* V, int dtype,
+                    void* stream) {
+  return dequantize_common(params, cache, seq_ids, positions, n_tokens, K, V, dtype, nullptr, 0,
+                           stream);
+}
+
+int isoq_dequantize_rope(const isoq_params* params, const isoq_cache* cache,
+                         const int32_t* seq_ids, const int32_t* positions, int n_tokens, void* K,
+                         void* V, int dtype, const float* rope_table, int rope_max_pos,
+                         void* stream) {
+  if (!rope_table || rope_max_pos < 1) return ISOQ_E_ARG;
+  return dequantize_common(params, cache, seq_ids, positions, n_tokens, K, V, dtype, rope_table,
+                           rope_max_pos, stream);
 }
 
 size_t isoq_rope_table_bytes(int d, int max_pos) {

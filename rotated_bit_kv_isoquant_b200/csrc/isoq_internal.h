@@ -41,6 +41,24 @@ struct QuantizeArgs {
   int rope_max_pos;
 };
 
+// Read-back of listed tokens; by value to the kernels.
+struct DequantizeArgs {
+  const float* mats;    // device [H][d/4][4][4]: block rotations as matrices
+  int bits, n_kv_heads, d;
+  const uint8_t* blocks;
+  const int32_t* page_table;
+  int n_pages, max_pages, n_seqs;
+  uint32_t* status;
+  const int32_t* seq_ids;
+  const int32_t* positions;
+  int n_tokens;
+  void* K;              // [n_tokens][n_kv_heads][d] of type dtype, or null
+  void* V;
+  int dtype;
+  const float* rope;    // optional [rope_max_pos][d/2][2]: taken off K
+  int rope_max_pos;
+};
+
 struct DecodeArgs {
   const float* params;  // the heads' 4x4 block matrices [n_kv_heads][d/4][16]
   int bits;             // bits per code (2, 3, 4)
@@ -69,6 +87,7 @@ cudaError_t launch_quantize_append(const QuantizeArgs& a, cudaStream_t stream, i
 // d = 128, bf16 / f16 inputs without RoPE: the WHT as a tensor-core product.
 bool use_quantize_tc(const QuantizeArgs& a);
 cudaError_t launch_quantize_tc(const QuantizeArgs& a, cudaStream_t stream, int n_sm);
+cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 // Merge of context-slice states [n_states][n_seqs][n_q_heads][d + 4] into the output.
 cudaError_t launch_merge_states(const float* params, int n_kv_heads, int d, int n_seqs,

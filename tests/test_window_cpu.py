@@ -91,3 +91,17 @@ def test_binding_checks_shapes_and_devices():
             call(None, _Cache, q, sl, 100, 16, 4, out, 1.0, ws)
     with pytest.raises(ValueError):
         iq.isoq_multi_token_attention_window(None, _Cache, Q, lens, 100, 16, 4, Q, 1.0, ws)
+
+
+def test_read_back_binding_checks():
+    class C:
+        d, n_kv_heads, blocks = 128, 2, torch.zeros(1)
+    i = torch.zeros(3, dtype=torch.int32)
+    K = torch.zeros(3, 2, 128)
+    for sid, pos, k, v in [(i, i, None, None), (i, i[:2], K, K), (i[None], i[None], K, K), (i, i, K[:2], K),
+                           (i, i, K, K.half()), (i, i, K[:, :1], None), (i, i, K.to("meta"), None)]:
+        with pytest.raises(ValueError):
+            iq.isoq_dequantize(None, C, sid, pos, k, v)
+    with pytest.raises(ValueError):
+        iq.isoq_dequantize_rope(None, C, i, i, K, K, torch.zeros(9, 32, 2))
+    assert LIB.isoq_dequantize(None, None, None, None, 1, None, None, 0, None) == iq.ISOQ_E_ARG
