@@ -6,6 +6,7 @@
 // off again: (a, b) = dims (i, i + d/2) -> (a cos + b sin, b cos - a sin).
 #include "isoq_check.cuh"
 #include "isoq_common.cuh"
+#include "isoq_dequantize.cuh"
 #include "isoq_internal.h"
 #include "isoq_ptx.cuh"
 #include "isoq_vtile.cuh"
@@ -13,27 +14,6 @@
 namespace isoq {
 using namespace ptx;
 namespace {
-
-// The physical page of token i of the list, or -1 with the reason's status bit.
-__device__ __forceinline__ int find_page(const DequantizeArgs& a, int i, int& pos, bool report) {
-  const int s = __ldg(a.seq_ids + i);
-  pos = __ldg(a.positions + i);
-  uint32_t bad = 0;
-  int phys = -1;
-  if (s < 0 || s >= a.n_seqs) {
-    bad = ISOQ_ST_SEQ_RANGE;
-  } else if (pos < 0 || pos / kPage >= a.max_pages || (a.rope && pos >= a.rope_max_pos)) {
-    bad = ISOQ_ST_POS_RANGE;
-  } else {
-    phys = __ldg(a.page_table + (size_t)s * a.max_pages + pos / kPage);
-    if (phys < 0 || phys >= a.n_pages) {
-      bad = ISOQ_ST_PAGE_RANGE;
-      phys = -1;
-    }
-  }
-  if (bad && report) set_status(a.status, bad);
-  return phys;
-}
 
 template <typename T, int E>
 __device__ __forceinline__ void store_vec(T* p, const float (&v)[E]) {
@@ -69,9 +49,14 @@ __global__ void __launch_bounds__(kDqWarps * 32) dequantize_warp_kernel(const De
   __syncthreads();
   const int h = blockIdx.y, i = blockIdx.x * kDqWarps + (tid >> 5);
   if (i >= a.n_tokens) return;
-  int pos;
-  const int phys = find_page(a, i, pos, lane == 0 && h == 0);
-  if (phys < 0) return;
+  uint32_t bad;
+  const int pos = __ldg(a.positions + i);
+  const long long entry = page_entry(a, __ldg(a.seq_ids + i), pos, bad);
+  const int phys = entry < 0 ? -1 : valid_page(a, __ldg(a.page_table + entry), bad);
+  if (phys < 0) {
+    if (lane == 0 && h == 0) set_status(a.status, bad);
+    return;
+  }
   const int slot = pos & (kPage - 1);
   const uint8_t* blk = a.blocks + ((size_t)phys * a.n_kv_heads + h) * BB;
   float M[NB][16];
@@ -94,14 +79,8 @@ __global__ void __launch_bounds__(kDqWarps * 32) dequantize_warp_kernel(const De
       const int go = vt_group_off(D, B, t, dim / 8);
       if (!in_bounds(go + 12 <= kPage * CB, a.status)) continue;
       const uint32_t* g = reinterpret_cast<const uint32_t*>(codes + go);
-      uint32_t w[3];
-#pragma unroll
-      for (int b = 0; b < 3; ++b) w[b] = __ldg(g + b) >> (4 * j);
-      const uint32_t sp = spare_codes(w[0], w[1], w[2]);
-      // dims 2b, 2b + 1 of the unit: nibbles 0 and 4 of word b (the spare unit for b = 3)
-      auto pair = [](uint32_t x) { return (x & 7u) | ((x >> 12) & 0x70u); };
-      const uint32_t lo = pair(w[0]) | pair(w[1]) << 8, hi = pair(w[2]) | pair(sp) << 8;
-      f = E == 8 ? lo | hi << 16 : ((lane & 1) ? hi : lo);
+      const uint32_t U = member_unit(__ldg(g), __ldg(g + 1), __ldg(g + 2), j);
+      f = U >> (E == 4 ? 16 * (lane & 1) : 0);
     } else if (BITS == 3) {
       const int go = slot * CB + dim / 32 * 12;
       if (!in_bounds(go + 12 <= kPage * CB, a.status)) continue;
@@ -166,7 +145,8 @@ cudaError_t launch_t(const DequantizeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream) {
+cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream, int n_sm) {
+  if (use_dequantize_tc(a)) return launch_dequantize_tc(a, stream, n_sm);
   if (a.d == 256) return launch_t<256, 3>(a, stream);
   switch (a.bits) {
     case 2: return launch_t<128, 2>(a, stream);

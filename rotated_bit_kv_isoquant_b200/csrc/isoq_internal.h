@@ -44,6 +44,7 @@ struct QuantizeArgs {
 // Read-back of listed tokens; by value to the kernels.
 struct DequantizeArgs {
   const float* mats;    // device [H][d/4][4][4]: block rotations as matrices
+  const void* rot;      // device: the inverse rotation's binary16 operands (isoq_api.cu)
   int bits, n_kv_heads, d;
   const uint8_t* blocks;
   const int32_t* page_table;
@@ -87,7 +88,19 @@ cudaError_t launch_quantize_append(const QuantizeArgs& a, cudaStream_t stream, i
 // d = 128, bf16 / f16 inputs without RoPE: the WHT as a tensor-core product.
 bool use_quantize_tc(const QuantizeArgs& a);
 cudaError_t launch_quantize_tc(const QuantizeArgs& a, cudaStream_t stream, int n_sm);
-cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream);
+cudaError_t launch_dequantize(const DequantizeArgs& a, cudaStream_t stream, int n_sm);
+// 16-bit outputs: the inverse rotation as a tensor-core product.
+bool use_dequantize_tc(const DequantizeArgs& a);
+cudaError_t launch_dequantize_tc(const DequantizeArgs& a, cudaStream_t stream, int n_sm);
+// Dim of column n of the 128-wide half q of that product.  The two 64-column halves hold the
+// dims (i, i + d/2) of the rotary pairs, so that one CTA holds both; inside a half the order
+// is the accumulator fragments': lane t of a quad holds columns 8 j + 2 t, + 1 (j = 0..7),
+// which are made 16 consecutive dims, a 32-byte sector of a 16-bit output row.
+constexpr int read_column(int d, int q, int n) {
+  const int m = n & 63, in_half = 16 * ((m >> 1) & 3) + 2 * (m >> 3) + (m & 1);
+  return (d == 128 ? (n >> 6) * 64 : 64 * q + (n >> 6) * 128) + in_half;
+}
+constexpr float kRotScale = 1024.0f;  // keeps both binary16 parts of R out of the subnormals
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 // Merge of context-slice states [n_states][n_seqs][n_q_heads][d + 4] into the output.
 cudaError_t launch_merge_states(const float* params, int n_kv_heads, int d, int n_seqs,

@@ -117,6 +117,44 @@ def test_token_lists(oracle, d, bits, out):
         s.check(oracle, at, out)
 
 
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+@pytest.mark.parametrize("rope", [False, True])
+@pytest.mark.parametrize("d,bits,rot", FORMATS)
+def test_long_lists(oracle, d, bits, rot, rope, out):
+    """Enough vectors for the tensor-core kernel: runs that start on and off a 16-slot block,
+    any order, a ragged end, one side alone."""
+    s = Store([1400, 700, 65], 4, d, bits, rot, seed=21, rope=rope)
+    g = torch.Generator().manual_seed(5)
+    n = len(s.pos)
+    for at in [torch.arange(n), torch.arange(3, n - 2), torch.randperm(n, generator=g),
+               torch.cat([torch.arange(640, 1300), torch.arange(1400, 1400 + 577), torch.arange(64)])]:
+        s.check(oracle, at, out, rope=rope)
+    at = torch.cat([torch.arange(n), torch.arange(n)])
+    K, V = s.read(at, out, rope)
+    assert torch.equal(s.read(at, out, rope, v=False)[0], K) and torch.equal(s.read(at, out, rope, k=False)[1], V)
+    sid, pos = s.sid.clone(), s.pos.clone()
+    s.sid[7], s.pos[1500], s.pos[n - 1] = 9, -4, 10 ** 6
+    bad = s.read(at, out, rope, sentinel=5.0)
+    assert iq.isoq_get_status(s.cache) == iq.ISOQ_ST_SEQ_RANGE | iq.ISOQ_ST_POS_RANGE
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[[7, 1500, n - 1]] = False
+    keep = torch.cat([keep, keep]).cuda()
+    for got, want in zip(bad, (K, V)):
+        assert torch.equal(got[keep], want[keep]) and bool((got[~keep] == 5.0).all())
+
+
+def test_long_list_into_rows_that_are_not_sector_aligned(oracle):
+    """A 16-byte aligned output is enough: the sectors are then written in two halves."""
+    s = Store([1400, 700], 4)
+    at = torch.arange(2100)
+    want = s.read(at, "bf16")
+    raw = torch.zeros(2100 * 4 * 128 + 8, dtype=torch.bfloat16, device="cuda")
+    K = raw[8:].view(2100, 4, 128)
+    assert K.data_ptr() % 32 == 16
+    iq.isoq_dequantize(s.params, s.cache, s.sid.cuda(), s.pos.cuda(), K, None)
+    assert torch.equal(K, want[0])
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("d,bits,H", [(128, 3, 1), (256, 3, 3), (128, 2, 8), (128, 4, 2)])
 def test_rope_taken_off(oracle, d, bits, H, out):
