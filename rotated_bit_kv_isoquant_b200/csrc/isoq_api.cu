@@ -139,13 +139,15 @@ struct SplitPlan {
 // Context chunking for the decode kernel: about ISOQ_DEC_WAVES waves of (chunk, KV head,
 // query-head block, sequence) CTAs at the kernel's resident CTAs per SM, each chunk a whole
 // number of pages and at least min_pages pages when the context allows.
-SplitPlan plan_pages(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_pages, int n_q) {
+SplitPlan plan_pages(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_pages, int n_q,
+                     bool windowed) {
   const int group = n_kv_heads > 0 ? n_q_heads / n_kv_heads : 1;
   // the multi-token kernels (64 or 128 rows per CTA, 2 CTAs per SM) when a chunk gives a
   // KV head at least 16 rows; else the per-row kernel (8 rows per CTA)
-  const bool shared_mq = isoq::shared_page_rows(d, n_q, group);
+  const bool shared_mq = d == 128 && n_q > 1 && (long long)n_q * group >= 16 && !windowed;
   const int n_sm = sm_count() * (shared_mq ? 2 : isoq::decode_i8_resident_ctas(d));
-  const int rows_per_cta = isoq::rows_per_cta(d, n_q, group);
+  const int rows_per_cta = shared_mq ? isoq::attention_rows_per_cta(d, n_q, group)
+                                     : isoq::decode_rows_per_block(d, n_q, group);
   // pages per CTA worth a launch: the tensor-memory kernel rotates 128 queries per CTA
   const int min_pages = shared_mq ? (rows_per_cta == 128 ? 16 : 4) : ISOQ_DEC_MIN_PAGES;
   const long long units =
@@ -170,7 +172,7 @@ int pages_of(int len) {
 
 SplitPlan plan_splits(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_seq_len,
                       int n_q = 1) {
-  return plan_pages(n_seqs, n_q_heads, n_kv_heads, d, pages_of(max_seq_len), n_q);
+  return plan_pages(n_seqs, n_q_heads, n_kv_heads, d, pages_of(max_seq_len), n_q, false);
 }
 
 // Most pages that the rows of one CTA can see with a window of W tokens and S sinks: a CTA
@@ -179,7 +181,8 @@ SplitPlan plan_splits(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_
 int window_pages(int n_q_heads, int n_kv_heads, int d, int max_seq_len, int n_q, int window,
                  int n_sinks) {
   const long long G = n_q_heads / n_kv_heads > 0 ? n_q_heads / n_kv_heads : 1;
-  const long long R = isoq::rows_per_cta(d, n_q, (int)G);
+  const long long R = isoq::use_window_tc(d, n_q, (int)G) ? isoq::window_tc_rows(n_q * (int)G)
+                                                         : isoq::decode_rows_per_block(d, n_q, (int)G);
   const long long span = n_q < (R + G - 2) / G + 1 ? n_q : (R + G - 2) / G + 1;
   const long long pages = ((long long)n_sinks + ISOQ_PAGE_SIZE - 1) / ISOQ_PAGE_SIZE +
                           ((long long)window + span - 1 + ISOQ_PAGE_SIZE - 2) / ISOQ_PAGE_SIZE + 1;
@@ -189,8 +192,28 @@ int window_pages(int n_q_heads, int n_kv_heads, int d, int max_seq_len, int n_q,
 
 SplitPlan plan_window(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_seq_len, int n_q,
                       int window, int n_sinks) {
-  return plan_pages(n_seqs, n_q_heads, n_kv_heads, d,
-                    window_pages(n_q_heads, n_kv_heads, d, max_seq_len, n_q, window, n_sinks), n_q);
+  const int pages = window_pages(n_q_heads, n_kv_heads, d, max_seq_len, n_q, window, n_sinks);
+  const int G = n_q_heads / n_kv_heads > 0 ? n_q_heads / n_kv_heads : 1;
+  if (!isoq::use_window_tc(d, n_q, G))
+    return plan_pages(n_seqs, n_q_heads, n_kv_heads, d, pages, n_q, true);
+  // The tensor-memory kernel runs one CTA per SM: the number of chunks with the smallest
+  // (rounds of CTAs) x (pages of a chunk + its start and end), in units of a page's time.  A
+  // start and end (128 or 256 queries rotated, the rows written) cost about 8 pages; more than
+  // one chunk adds the combine.
+  const int per = isoq::window_tc_rows(n_q * G), slots = sm_count();
+  const long long units = (long long)n_seqs * n_kv_heads * (((long long)n_q * G + per - 1) / per);
+  int best = 1;
+  long long best_cost = -1;
+  for (int s = 1; s <= pages && s <= 64; ++s) {
+    const long long cost = ((units * s + slots - 1) / slots) * ((pages + s - 1) / s + 8) + (s > 1 ? 4 : 0);
+    if (best_cost < 0 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  int pps = (pages + best - 1) / best;
+  if (pps > isoq::kMaxPagesPerSplit) pps = isoq::kMaxPagesPerSplit;
+  return SplitPlan{(pages + pps - 1) / pps, pps};
 }
 
 int check_cache(const isoq_cache* c, const isoq_params* p) {
@@ -654,6 +677,7 @@ int window_common(const isoq_params* params, const isoq_cache* cache, const void
                   size_t workspace_bytes, void* stream) {
   if (window < 1 || n_sinks < 0 || !valid_dtype(out_dtype)) return ISOQ_E_ARG;
   if (!out && n_seqs > 0 && n_q_heads > 0) return ISOQ_E_ARG;
+  if (((uintptr_t)out & 15u) != 0) return ISOQ_E_ARG;  // rows are written in 16-byte pieces
   return decode_common_impl(params, cache, Q, q_dtype, n_seqs, n_q, n_q_heads, seq_lens,
                             max_seq_len, window, n_sinks, out, out_dtype, nullptr, scale, workspace,
                             workspace_bytes, stream);

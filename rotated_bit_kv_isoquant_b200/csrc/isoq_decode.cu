@@ -174,10 +174,13 @@ static cudaError_t launch_combine(dim3 grid, cudaStream_t stream, bool dependent
 
 template <int D>
 static cudaError_t launch_dq(const DecodeArgs& a, cudaStream_t stream) {
-  bool combined = false;  // a single-chunk 3-bit decode writes the output itself
-  cudaError_t e = use_shared_mq(a) ? launch_decode_split_mq(a, stream)
-                  : a.bits == 3    ? launch_decode_split_i8(a, stream, &combined)
-                                   : launch_decode_split_mma(a, stream);
+  bool combined = false;  // single-chunk calls of some kernels write the output themselves
+  const bool window_tc = a.window > 0 && use_window_tc(a.d, a.n_q, a.n_q_heads / a.n_kv_heads);
+  cudaError_t e = window_tc                          ? launch_window_tc(a, stream)
+                  : a.window == 0 && use_shared_mq(a) ? launch_decode_split_mq(a, stream)
+                  : a.bits == 3                      ? launch_decode_split_i8(a, stream, &combined)
+                                                     : launch_decode_split_mma(a, stream);
+  if (window_tc) combined = a.n_splits == 1;
   if (e != cudaSuccess) return e;
   if (combined) return cudaSuccess;
   const int rows = a.n_q * a.n_q_heads;

@@ -26,7 +26,6 @@
 #include "isoq_common.cuh"
 #include "isoq_internal.h"
 #include "isoq_ptx.cuh"
-#include "isoq_window.cuh"
 #include "isoq_vtile.cuh"
 
 namespace isoq {
@@ -70,15 +69,13 @@ __device__ __forceinline__ uint32_t tile_off(int tk, int c) {
   return (uint32_t)(tk * (kMqD * 2) + ((c ^ (tk & 7)) << 4));
 }
 
-// WIN: sliding-window attention with sinks (isoq_window.cuh).
-template <typename TQ, int BITS, bool WIN>
+template <typename TQ, int BITS>
 __global__ void __launch_bounds__(kMqWarps * 32, 2)
     decode_mq_kernel(const float* __restrict__ params, const uint8_t* __restrict__ blocks,
                      const int32_t* __restrict__ page_table, int n_pages, int max_pages, int H,
                      const TQ* __restrict__ Q, int n_q_heads, int n_q,
                      const int32_t* __restrict__ seq_lens, float scale, int pages_per_split,
-                     int n_splits, float* __restrict__ partials, uint32_t* status,
-                     const WinArgs win) {
+                     int n_splits, float* __restrict__ partials, uint32_t* status) {
   using SM = MqSmem<BITS>;
   constexpr int D = kMqD, E = D / 32, NB = E / 4, KS = kMqKS, PS = D + 4;
   constexpr int CB = code_bytes(D, BITS), BB = block_bytes(D, BITS), W = BITS;
@@ -100,8 +97,11 @@ __global__ void __launch_bounds__(kMqWarps * 32, 2)
   const int row0 = rg * 64;                       // first row (of this KV head's) here
   const int nh = min(64, n_rows - row0);          // rows handled here
 
-  const int len = clamp_len<WIN>(__ldg(seq_lens + s), max_pages, win,
-                                 tid == 0 && split == 0 && blockIdx.y == 0, status);
+  int len = __ldg(seq_lens + s);
+  if (len > max_pages * kPage) {
+    if (tid == 0 && split == 0 && blockIdx.y == 0) set_status(status, ISOQ_ST_LEN_RANGE);
+    len = max_pages * kPage;
+  }
   // row r (0..63) = pair R = row0 + r: query token R / G, head hk * G + R % G; causal
   // limit len - n_q + 1 + token
   if (tid < 64) {
@@ -110,9 +110,8 @@ __global__ void __launch_bounds__(kMqWarps * 32, 2)
   }
   auto lim_of = [&](int r) { return max(0, min(len, len - n_q + 1 + (row0 + r) / G)); };
   const int lim_hi = lim_of(nh - 1), lim_lo = lim_of(0);
-  const WinPages<WIN> wp(win, lim_lo, lim_hi);
-  const int p_begin = split * pages_per_split;  // slots of the pages to visit
-  const int p_end = min(wp.n_slots, p_begin + pages_per_split);
+  const int p_begin = split * pages_per_split;
+  const int p_end = min((lim_hi + kPage - 1) / kPage, p_begin + pages_per_split);
   float* out_base = partials + ((size_t)s * n_q * n_q_heads) * n_splits * PS + (size_t)split * PS;
   __syncthreads();
   if (p_begin >= p_end) {  // empty chunk: m = -inf, l = 0, acc = 0
@@ -129,8 +128,7 @@ __global__ void __launch_bounds__(kMqWarps * 32, 2)
   const int n_my = p_end - p_begin;
   auto issue = [&](int k) {  // thread 0
     const int st = k & 1;
-    const int pg = wp.page(p_begin + k);
-    const int phys = in_bounds(pg < max_pages, status) ? __ldg(pt_row + pg) : -1;
+    const int phys = in_bounds(p_begin + k < max_pages, status) ? __ldg(pt_row + p_begin + k) : -1;
     uint64_t* bar = bars + st;
     if (phys >= 0 && phys < n_pages) {
       mbar_expect_tx(bar, BB);
@@ -198,7 +196,6 @@ __global__ void __launch_bounds__(kMqWarps * 32, 2)
   // this warp's two row-blocks: b = 2 warp + {0, 1}; lane's rows g of each
   const int rbA = 2 * warp, rbB = rbA + 1;
   const int limA = lim_of(8 * rbA + g), limB = lim_of(8 * rbB + g);
-  const int loA = win_lo<WIN>(win, limA), loB = win_lo<WIN>(win, limB);
   const bool warp_active = 8 * rbA < nh;
   float m2[2] = {-CUDART_INF_F, -CUDART_INF_F}, lsum[2] = {0.f, 0.f};
   float sigma = 0.f, inv_sigma = 0.f;
@@ -289,7 +286,7 @@ __global__ void __launch_bounds__(kMqWarps * 32, 2)
       }
       dequant(k + 1);
     }
-    const int pg = wp.page(p_begin + k);
+    const int pg = p_begin + k;
     const int phys = in_bounds(pg < max_pages, status) ? __ldg(pt_row + pg) : -1;
     const bool page_ok = phys >= 0 && phys < n_pages;
     const int tok0 = pg * kPage;
@@ -298,7 +295,7 @@ __global__ void __launch_bounds__(kMqWarps * 32, 2)
 
     if (warp_active) {
       // a page whose 64 tokens are valid for every row of the CTA needs no masking
-      const bool full = page_ok && tok0 + kPage <= lim_lo && wp.page_full(win, tok0);
+      const bool full = page_ok && tok0 + kPage <= lim_lo;
 #pragma unroll 1
       for (int hb = 0; hb < 64; hb += 32) {
         // ---- a7: scores of both row-blocks for tokens hb + 8n + (0..7), n = 0..3 --------
@@ -343,11 +340,10 @@ __global__ void __launch_bounds__(kMqWarps * 32, 2)
             float nvx = nrm[64 + tk];
             float s0 = (C[0][n][e] + C[0][n][e + 2]) * nk, s1 = (C[1][n][e] + C[1][n][e + 2]) * nk;
             if (!full) {
-              const int tok = tok0 + tk;
-              const bool ok = page_ok && tok < lim_hi && wp.any_sees(win, tok);
+              const bool ok = page_ok && tok0 + tk < lim_hi;
               nvx = ok ? nvx : 0.f;
-              s0 = ok && tok < limA && win_sees<WIN>(win, loA, tok) ? s0 : -CUDART_INF_F;
-              s1 = ok && tok < limB && win_sees<WIN>(win, loB, tok) ? s1 : -CUDART_INF_F;
+              s0 = ok && tok0 + tk < limA ? s0 : -CUDART_INF_F;
+              s1 = ok && tok0 + tk < limB ? s1 : -CUDART_INF_F;
             }
             nvv[n][e] = nvx;
             sv[0][n][e] = s0;
@@ -477,7 +473,7 @@ __global__ void __launch_bounds__(kMqWarps * 32, 2)
   }
 }
 
-template <typename TQ, int BITS, bool WIN>
+template <typename TQ, int BITS>
 cudaError_t launch_mq_t(const DecodeArgs& a, cudaStream_t stream) {
   using SM = MqSmem<BITS>;
   static unsigned long long attr_set = 0;
@@ -485,32 +481,26 @@ cudaError_t launch_mq_t(const DecodeArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !((attr_set >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(decode_mq_kernel<TQ, BITS, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(decode_mq_kernel<TQ, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              SM::kBytes);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
   const int G = a.n_q_heads / a.n_kv_heads;
   dim3 grid(a.n_splits, a.n_kv_heads * ((a.n_q * G + 63) / 64), a.n_seqs);
-  decode_mq_kernel<TQ, BITS, WIN><<<grid, kMqWarps * 32, SM::kBytes, stream>>>(
+  decode_mq_kernel<TQ, BITS><<<grid, kMqWarps * 32, SM::kBytes, stream>>>(
       a.params, a.blocks, a.page_table, a.n_pages, a.max_pages, a.n_kv_heads,
       static_cast<const TQ*>(a.Q), a.n_q_heads, a.n_q, a.seq_lens, a.scale, a.pages_per_split,
-      a.n_splits, a.partials, a.status, win_args(a));
+      a.n_splits, a.partials, a.status);
   return cudaGetLastError();
-}
-
-template <typename TQ, int BITS>
-cudaError_t launch_mq_q(const DecodeArgs& a, cudaStream_t stream) {
-  return a.window > 0 ? launch_mq_t<TQ, BITS, true>(a, stream)
-                      : launch_mq_t<TQ, BITS, false>(a, stream);
 }
 
 template <int BITS>
 cudaError_t launch_mq_b(const DecodeArgs& a, cudaStream_t stream) {
   switch (a.q_dtype) {
-    case ISOQ_F32: return launch_mq_q<float, BITS>(a, stream);
-    case ISOQ_BF16: return launch_mq_q<__nv_bfloat16, BITS>(a, stream);
-    case ISOQ_F16: return launch_mq_q<__half, BITS>(a, stream);
+    case ISOQ_F32: return launch_mq_t<float, BITS>(a, stream);
+    case ISOQ_BF16: return launch_mq_t<__nv_bfloat16, BITS>(a, stream);
+    case ISOQ_F16: return launch_mq_t<__half, BITS>(a, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -30,8 +30,8 @@
 #include "isoq_check.cuh"
 #include "isoq_common.cuh"
 #include "isoq_internal.h"
+#include "isoq_pagetile.cuh"
 #include "isoq_ptx.cuh"
-#include "isoq_window.cuh"
 #include "isoq_vtile.cuh"
 #include "isoq_tc.cuh"
 
@@ -67,24 +67,16 @@ struct MqtcSmem {
   static constexpr int kBytes = kOffRow + kXRows * 4;
 };
 
-__device__ __forceinline__ void st_v4(uint32_t addr, const uint32_t (&o)[4]) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(o[0]), "r"(o[1]),
-               "r"(o[2]), "r"(o[3])
-               : "memory");
-}
-
-// WIN: sliding-window attention with sinks (isoq_window.cuh).
-template <typename TQ, int BITS, bool WIN>
+template <typename TQ, int BITS>
 __global__ void __launch_bounds__(kXRows, 2)
     decode_mqtc_kernel(const float* __restrict__ params, const uint8_t* __restrict__ blocks,
                        const int32_t* __restrict__ page_table, int n_pages, int max_pages,
                        int H, const TQ* __restrict__ Q, int n_q_heads, int n_q,
                        const int32_t* __restrict__ seq_lens, float scale, int pages_per_split,
-                       int n_splits, float* __restrict__ partials, uint32_t* status,
-                     const WinArgs win) {
+                       int n_splits, float* __restrict__ partials, uint32_t* status) {
   using SM = MqtcSmem<BITS>;
   constexpr int D = kXD, E = D / 32, NB = E / 4, PS = D + 4;
-  constexpr int CB = code_bytes(D, BITS), BB = block_bytes(D, BITS), W = BITS;
+  constexpr int BB = block_bytes(D, BITS);
   constexpr float ALPHA = alpha_of<BITS>();
   constexpr uint32_t kIdS = tc::idesc_f16(128, 64, false, false);   // scores
   constexpr uint32_t kIdO = tc::idesc_f16(128, 128, false, true);   // value product
@@ -108,8 +100,11 @@ __global__ void __launch_bounds__(kXRows, 2)
   const int row0 = rg * kXRows;
   const int nh = min(kXRows, n_rows - row0);  // rows handled here
 
-  const int len = clamp_len<WIN>(__ldg(seq_lens + s), max_pages, win,
-                                 tid == 0 && split == 0 && blockIdx.y == 0, status);
+  int len = __ldg(seq_lens + s);
+  if (len > max_pages * kPage) {
+    if (tid == 0 && split == 0 && blockIdx.y == 0) set_status(status, ISOQ_ST_LEN_RANGE);
+    len = max_pages * kPage;
+  }
   // row r = pair R = row0 + r: query token R / G, head hk * G + R % G, which sits at
   // position len - n_q + R / G and attends the tokens before and at it
   {
@@ -119,11 +114,8 @@ __global__ void __launch_bounds__(kXRows, 2)
   auto lim_of = [&](int r) { return max(0, min(len, len - n_q + 1 + (row0 + r) / G)); };
   const int lim_hi = lim_of(nh - 1), lim_lo = lim_of(0);
   const int my_lim = tid < nh ? lim_of(tid) : lim_hi;
-  const int my_lo = win_lo<WIN>(win, my_lim);
-  auto sees = [&](int tok) { return tok < my_lim && win_sees<WIN>(win, my_lo, tok); };
-  const WinPages<WIN> wp(win, lim_lo, lim_hi);
-  const int p_begin = split * pages_per_split;  // slots of the pages to visit
-  const int p_end = min(wp.n_slots, p_begin + pages_per_split);
+  const int p_begin = split * pages_per_split;
+  const int p_end = min((lim_hi + kPage - 1) / kPage, p_begin + pages_per_split);
   float* out_base = partials + ((size_t)s * n_q * n_q_heads) * n_splits * PS + (size_t)split * PS;
   __syncthreads();
   if (p_begin >= p_end) {  // empty chunk: m = -inf, l = 0, acc = 0
@@ -141,8 +133,7 @@ __global__ void __launch_bounds__(kXRows, 2)
   if (warp == 0) tc::alloc(tmem_slot, kXCols);
   auto issue = [&](int k) {  // thread 0
     const int st = k & 1;
-    const int pg = wp.page(p_begin + k);
-    const int phys = in_bounds(pg < max_pages, status) ? __ldg(pt_row + pg) : -1;
+    const int phys = in_bounds(p_begin + k < max_pages, status) ? __ldg(pt_row + p_begin + k) : -1;
     if (phys >= 0 && phys < n_pages) {
       mbar_expect_tx(bars + st, BB);
       bulk_copy(smem + SM::kOffRing + st * BB, blocks + ((size_t)phys * H + hk) * BB, BB, bars + st);
@@ -213,75 +204,17 @@ __global__ void __launch_bounds__(kXRows, 2)
   int k = 0;
   // dequantise K_hat (kv = 0) or V_hat (kv = 1) of the page in ring stage st into its tile
   auto dequant = [&](int st, int kv) {
-    const uint8_t* blk = smem + SM::kOffRing + st * BB;
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int u = tid + 128 * hf;
-      if (BITS == 3 && kv == 1) {
-        // V tile layout: u = (block, quad, 8-dim unit) group of four tokens.  Lanes 4m ..
-        // 4m+3 take quads 0-3 of one unit, so a warp's 12-byte group loads hit 32 distinct
-        // banks.  A member's 16-byte tile row sits at chunk (2 quad + member bit 0) % 8 of
-        // a 128-byte line, the same line for every member of a unit; lanes with an odd unit
-        // store their members in the order 1 0 3 2 (nibbles swapped within each byte of
-        // the words), so each quarter-warp's stores cover the 8 chunks once.
-        const int t4 = u & 3, un = (u >> 2) & 15, B = u >> 6, jf = un & 1;
-        const uint32_t* wp = reinterpret_cast<const uint32_t*>(
-            blk + v_codes_off(D, BITS) + vt_group_off(D, B, t4, un));
-        if (!in_bounds(vt_group_off(D, B, t4, un) + 12 <= kPage * CB, status)) continue;
-        const int sh = 4 * jf;
-        uint32_t w3[3];
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const uint32_t x = wp[i];
-          w3[i] = ((x >> sh) & 0x0F0F0F0Fu) | ((x << sh) & 0xF0F0F0F0u);
-        }
-        uint32_t o[4][4];
-        vdeq_group(w3[0], w3[1], w3[2], tl0, tl1, th0, th1, o);  // o[j]: member j ^ jf
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int tkj = vt_member_slot(B, t4, j ^ jf);
-          const int vo = (tkj >> 3) * 2048 + un * 128 + (tkj & 7) * 16;
-          if (!in_bounds(vo + 16 <= SM::kOffRing - SM::kOffV, status)) continue;
-          st_v4(sV + vo, o[j]);
-        }
-        continue;
-      }
-      // token, 32-dim group: a warp takes 8 tokens x 4 groups, so its 32-bit code loads
-      // (word 12 tk + 3 q + i) hit 32 distinct banks and each quarter-warp's 16-byte tile
-      // stores 8 distinct bank groups (tk % 8)
-      const int tk = 8 * (u >> 5) + (u & 7), q = (u >> 3) & 3;
-      const uint32_t* wp = reinterpret_cast<const uint32_t*>(
-                               blk + (kv ? v_codes_off(D, BITS) : 0) + tk * CB) + W * q;
-      if (!in_bounds(tk * CB + 4 * W * (q + 1) <= kPage * CB, status)) continue;
-      uint32_t w[W];
-#pragma unroll
-      for (int i = 0; i < W; ++i) w[i] = wp[i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t o[4];
-        kdeq<BITS>(w, j, tl0, tl1, th0, th1, o);  // dims 32q + 8j .. +7 of token tk
-        const int c = 4 * q + j;
-        const uint32_t to = kv ? (tk >> 3) * 2048 + c * 128 + (tk & 7) * 16
-                               : c * 1024 + (tk >> 3) * 128 + (tk & 7) * 16;
-        if (!in_bounds(to + 16 <= (kv ? SM::kOffRing - SM::kOffV : SM::kOffV - SM::kOffK), status))
-          continue;
-        const uint32_t addr = (kv ? sV : sK) + to;
-        st_v4(addr, o);
-      }
-    }
+    page_tile<BITS>(smem + SM::kOffRing + st * BB, kv, tid, kv ? sV : sK, tl0, tl1, th0, th1, status);
   };
 
   // Per page k: K_hat(k) -> tile; S(k) issued; V_hat(k) -> tile while S(k) runs; softmax;
   // O += P' V_hat issued, which runs while the next page's K_hat is dequantised.
   // page-table entry of the next page, loaded one page ahead (off the per-page chain)
-  auto phys_of = [&](int kk) {
-    const int pg = wp.page(p_begin + kk);
-    return in_bounds(pg < max_pages, status) ? __ldg(pt_row + pg) : -1;
-  };
-  int phys_nx = n_my > 0 ? phys_of(0) : -1;
+  int phys_nx = n_my > 0 && in_bounds(p_begin < max_pages, status) ? __ldg(pt_row + p_begin) : -1;
   for (; k < n_my; ++k) {
     const int phys = phys_nx;
-    if (k + 1 < n_my) phys_nx = phys_of(k + 1);
+    if (k + 1 < n_my)
+      phys_nx = in_bounds(p_begin + k + 1 < max_pages, status) ? __ldg(pt_row + p_begin + k + 1) : -1;
     // Three CTA barriers per page; every other hand-off is a thread's own mbarrier wait.
     // The K tile is free: S(k-1) completed before this thread's softmax read it.
     bool ok = mbar_wait(bars + (k & 1), (k >> 1) & 1);
@@ -308,10 +241,10 @@ __global__ void __launch_bounds__(kXRows, 2)
     // thread's own wait); the norms of page k-1 were read before the last barrier
     ok = k == 0 || mbar_wait(bar_pv, (k - 1) & 1);
     if (ok) dequant(k & 1, 1);
-    const int pg = wp.page(p_begin + k);
+    const int pg = p_begin + k;
     const bool page_ok = phys >= 0 && phys < n_pages;
     const int tok0 = pg * kPage;
-    const bool full = page_ok && tok0 + kPage <= lim_lo && wp.page_full(win, tok0);
+    const bool full = page_ok && tok0 + kPage <= lim_lo;
     // norms: nrm[j] = |k_j| kf; nrm[64 + j] = |v_j| / sigma', where sigma' is the CTA's
     // V-norm reference (shared by all rows: it only scales the weights), raised when a
     // token valid for some row has |v| > kSigmaSlack sigma; computed by warps 2 and 3
@@ -322,7 +255,7 @@ __global__ void __launch_bounds__(kXRows, 2)
       } else {
         const int j = tid - 64;
         float nv = half_at(blk + v_norm_off(D, BITS) + 2 * j);
-        nv = page_ok && tok0 + j < lim_hi && wp.any_sees(win, tok0 + j) ? nv : 0.f;
+        nv = page_ok && tok0 + j < lim_hi ? nv : 0.f;
         float pm = nv;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, o));
@@ -373,7 +306,7 @@ __global__ void __launch_bounds__(kXRows, 2)
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
           float sc = x[j] * nrm[j];
-          if constexpr (!FULL) sc = page_ok && sees(tok0 + j) ? sc : -CUDART_INF_F;
+          if constexpr (!FULL) sc = page_ok && tok0 + j < my_lim ? sc : -CUDART_INF_F;
           x[j] = sc;
           tm[j & 3] = fmaxf(tm[j & 3], sc);
         }
@@ -400,7 +333,7 @@ __global__ void __launch_bounds__(kXRows, 2)
           for (int e = 0; e < 4; ++e) {
             const int j = j4 + e;
             float a = av[e];
-            if constexpr (!FULL) a = page_ok && sees(tok0 + j) ? a : -CUDART_INF_F;
+            if constexpr (!FULL) a = page_ok && tok0 + j < my_lim ? a : -CUDART_INF_F;
             x[j] = a;
             am[e] = fmaxf(am[e], a);
           }
@@ -518,7 +451,7 @@ __global__ void __launch_bounds__(kXRows, 2)
   }
 }
 
-template <typename TQ, int BITS, bool WIN>
+template <typename TQ, int BITS>
 cudaError_t launch_mqtc_t(const DecodeArgs& a, cudaStream_t stream) {
   using SM = MqtcSmem<BITS>;
   static unsigned long long attr_set = 0;
@@ -526,32 +459,26 @@ cudaError_t launch_mqtc_t(const DecodeArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !((attr_set >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(decode_mqtc_kernel<TQ, BITS, WIN>,
+    e = cudaFuncSetAttribute(decode_mqtc_kernel<TQ, BITS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
   const int G = a.n_q_heads / a.n_kv_heads;
   dim3 grid(a.n_splits, a.n_kv_heads * ((a.n_q * G + kXRows - 1) / kXRows), a.n_seqs);
-  decode_mqtc_kernel<TQ, BITS, WIN><<<grid, kXRows, SM::kBytes, stream>>>(
+  decode_mqtc_kernel<TQ, BITS><<<grid, kXRows, SM::kBytes, stream>>>(
       a.params, a.blocks, a.page_table, a.n_pages, a.max_pages, a.n_kv_heads,
       static_cast<const TQ*>(a.Q), a.n_q_heads, a.n_q, a.seq_lens, a.scale, a.pages_per_split,
-      a.n_splits, a.partials, a.status, win_args(a));
+      a.n_splits, a.partials, a.status);
   return cudaGetLastError();
-}
-
-template <typename TQ, int BITS>
-cudaError_t launch_mqtc_q(const DecodeArgs& a, cudaStream_t stream) {
-  return a.window > 0 ? launch_mqtc_t<TQ, BITS, true>(a, stream)
-                      : launch_mqtc_t<TQ, BITS, false>(a, stream);
 }
 
 template <int BITS>
 cudaError_t launch_mqtc_b(const DecodeArgs& a, cudaStream_t stream) {
   switch (a.q_dtype) {
-    case ISOQ_F32: return launch_mqtc_q<float, BITS>(a, stream);
-    case ISOQ_BF16: return launch_mqtc_q<__nv_bfloat16, BITS>(a, stream);
-    case ISOQ_F16: return launch_mqtc_q<__half, BITS>(a, stream);
+    case ISOQ_F32: return launch_mqtc_t<float, BITS>(a, stream);
+    case ISOQ_BF16: return launch_mqtc_t<__nv_bfloat16, BITS>(a, stream);
+    case ISOQ_F16: return launch_mqtc_t<__half, BITS>(a, stream);
   }
   return cudaErrorInvalidValue;
 }

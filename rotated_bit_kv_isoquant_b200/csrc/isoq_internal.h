@@ -145,15 +145,13 @@ inline int attention_rows_per_cta(int d, int n_q, int group) {
   return rows >= ISOQ_MQTC_MIN_ROWS ? 128 : 64;
 }
 
-// A chunk of query tokens that takes the kernels in which 64 or 128 rows share a page.
-inline bool shared_page_rows(int d, int n_q, int group) {
-  return d == 128 && n_q > 1 && (long long)n_q * group >= 16;
+// Windowed chunks with more than 32 rows per KV head (d = 128) take the tensor-memory kernel,
+// 128 rows a CTA or 256 where a KV head has more; the others the row-block kernels.
+inline bool use_window_tc(int d, int n_q, int group) {
+  return d == 128 && n_q > 1 && (long long)n_q * group > 32;
 }
-// Rows per CTA of the attention kernel that a call takes.
-inline int rows_per_cta(int d, int n_q, int group) {
-  return shared_page_rows(d, n_q, group) ? attention_rows_per_cta(d, n_q, group)
-                                         : decode_rows_per_block(d, n_q, group);
-}
+inline int window_tc_rows(int rows) { return rows > 128 ? 256 : 128; }
+cudaError_t launch_window_tc(const DecodeArgs& a, cudaStream_t stream);
 
 // Accessors of the opaque parameter handle (defined in isoq_api.cu).
 const float* params_device_mats(const struct ::isoq_params* p);  // [H][d/4][4][4]

@@ -1,0 +1,610 @@
+// Sliding-window attention of a chunk of query tokens with many rows per KV head (d = 128) on
+// the 5th-generation tensor cores, its steps on warps of their own.
+//
+// As in the other attention kernels the queries are rotated once, scores and value sum run on
+// codebook levels in the rotated space, and a row is a (query token, query head) pair; what a
+// row sees is isoq_window.cuh's.  One CTA per SM of 13 warps works on one context chunk of one
+// KV head:
+//   warps 8-11   take the page blocks from a 2-stage ring (1-D bulk copies) and dequantise
+//                K_hat and V_hat into two f16 operand tiles each, with the page's norms
+//   warp 12      one thread issues the products: scores S = Q~hi K_hat^T + Q~lo K_hat^T and
+//                O += P' V_hat, accumulators in tensor memory
+//   warps 0-3,   softmax: thread r owns row r of its half (tensor-memory lane r), reads its 64
+//   warps 4-7    scores, keeps its running maximum and sum, writes P' = p |v| / sigma
+// With more than 128 rows per KV head the two softmax halves hold two blocks of 128 rows and
+// share every page's tiles (256 rows for one dequantisation); with fewer both hold the same
+// rows and take the pages in turn, and their states are merged at the end.  So one half's
+// softmax runs while the other half's products do, and the next page is dequantised
+// meanwhile; all hand-offs are mbarriers with bounded waits, none a CTA barrier.
+//
+// The score queries keep an f16 high and low part, the weights P' are f16 with f32
+// accumulators, statistics are f32 (as in the multi-token kernel, whose error bounds hold).
+// A call whose rows' pages fit one chunk divides, rotates back and writes its output here: a
+// thread holds its whole row.  Otherwise partial states go to the combine.
+#include <math_constants.h>
+
+#include <type_traits>
+
+#include "isoq_check.cuh"
+#include "isoq_common.cuh"
+#include "isoq_internal.h"
+#include "isoq_pagetile.cuh"
+#include "isoq_ptx.cuh"
+#include "isoq_tc.cuh"
+#include "isoq_window.cuh"
+
+namespace isoq {
+using namespace ptx;
+namespace {
+
+constexpr int kWD = 128;
+constexpr int kWThreads = 13 * 32;
+// tensor-memory columns: S 64, P' 32 and O 128 of each half
+constexpr uint32_t kWCols = 512;
+__device__ __forceinline__ constexpr uint32_t col_s(int w) { return 64 * w; }
+__device__ __forceinline__ constexpr uint32_t col_p(int w) { return 128 + 32 * w; }
+__device__ __forceinline__ constexpr uint32_t col_o(int w) { return 256 + 128 * w; }
+
+enum Bar {  // mbarriers, two of each (by ring / tile stage, or by softmax half)
+  kRing = 0, kKFull = 2, kVFull = 4, kKFree = 6, kVFree = 8,
+  kSFull = 10, kSRead = 12, kPFull = 14, kPvDone = 16, kDrain = 18, kBars = 19
+};
+
+template <int BITS>
+struct WinSmem {
+  static constexpr int kBB = block_bytes(kWD, BITS);
+  // at 0: the queries, [2 halves][hi, lo] 32 KB, at the end the halves' merge
+  static constexpr int kOffK = 4 * 32768;               // [2] K_hat tiles
+  static constexpr int kOffV = kOffK + 2 * kPageTile;   // [2] V_hat tiles
+  static constexpr int kOffRing = kOffV + 2 * kPageTile;
+  static constexpr int kOffNorm = kOffRing + 2 * kBB;   // float [2][64 K | 64 V]
+  static constexpr int kOffMeta = kOffNorm + 2 * 128 * 4;  // float [2] sigma, int [2] page is valid
+  static constexpr int kOffRed = kOffMeta + 16;         // float [2]
+  static constexpr int kOffMl = kOffRed + 16;           // float2 [128]: m, l of the second half
+  static constexpr int kOffBar = kOffMl + 128 * 8;
+  static constexpr int kOffTmem = kOffBar + kBars * 8 + 8;
+  static constexpr int kBytes = kOffTmem + 16;
+  static_assert(kOffRing % 16 == 0 && kBB % 16 == 0 && kOffBar % 8 == 0 && kOffNorm % 16 == 0, "");
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+// One row of 128 rotated values: inverse blocks, WHT, factor; written in the caller's type.
+__device__ __forceinline__ void finish_row(float (&o)[kWD], const float* __restrict__ head_mats,
+                                           float factor, void* out, size_t at, int dtype) {
+#pragma unroll
+  for (int b = 0; b < kWD / 4; ++b) {
+    float M[16], y[4];
+    load_block_mat(head_mats, b, M);
+    mat_inv(M, o + 4 * b, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[4 * b + i] = y[i] * factor;
+  }
+#pragma unroll
+  for (int h = 1; h < kWD; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < kWD; i += 2 * h)
+#pragma unroll
+      for (int j = i; j < i + h; ++j) {
+        const float a = o[j], b = o[j + h];
+        o[j] = a + b;
+        o[j + h] = a - b;
+      }
+  if (dtype == ISOQ_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+#pragma unroll
+    for (int i = 0; i < kWD / 4; ++i)
+      p[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    return;
+  }
+  uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+#pragma unroll
+  for (int i = 0; i < kWD / 8; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = o[8 * i + 2 * e], b = o[8 * i + 2 * e + 1];
+      if (dtype == ISOQ_F16) {
+        w[e] = pack_f16x2(a, b);
+      } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        w[e] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    p[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <typename TQ, int BITS>
+__global__ void __launch_bounds__(kWThreads, 1)
+    window_tc_kernel(const float* __restrict__ params, const uint8_t* __restrict__ blocks,
+                     const int32_t* __restrict__ page_table, int n_pages, int max_pages, int H,
+                     const TQ* __restrict__ Q, int n_q_heads, int n_q,
+                     const int32_t* __restrict__ seq_lens, float scale, int pages_per_split,
+                     int n_splits, float* __restrict__ partials, void* __restrict__ out,
+                     uint32_t* status, const WinArgs win) {
+  using SM = WinSmem<BITS>;
+  constexpr int D = kWD, E = D / 32, PS = D + 4, BB = SM::kBB;
+  constexpr float ALPHA = alpha_of<BITS>();
+  constexpr uint32_t kIdS = tc::idesc_f16(128, 64, false, false);  // scores
+  constexpr uint32_t kIdO = tc::idesc_f16(128, 128, false, true);  // value product
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);
+  float* nrm = reinterpret_cast<float*>(smem + SM::kOffNorm);
+  float* sig = reinterpret_cast<float*>(smem + SM::kOffMeta);
+  int* valid = reinterpret_cast<int*>(smem + SM::kOffMeta) + 2;
+  float* red = reinterpret_cast<float*>(smem + SM::kOffRed);
+  float2* ml1 = reinterpret_cast<float2*>(smem + SM::kOffMl);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kOffTmem);
+  const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + SM::kOffK), sV = smem_u32(smem + SM::kOffV);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = blockIdx.x, s = blockIdx.z;
+  const int G = n_q_heads / H;
+  const int n_rows = n_q * G;
+  const bool two = n_rows > 128;                 // two row blocks that share the pages
+  const int rows_cta = two ? 256 : 128;
+  const int n_groups = (n_rows + rows_cta - 1) / rows_cta;
+  const int hk = blockIdx.y / n_groups, row0 = (blockIdx.y - hk * n_groups) * rows_cta;
+  const int nh = min(rows_cta, n_rows - row0);   // rows handled here
+  auto row_index = [&](int r) {                  // row of the sequence's output / partials
+    const int R = row0 + r;
+    return (R / G) * n_q_heads + hk * G + R % G;
+  };
+
+  const int len = clamp_len<true>(__ldg(seq_lens + s), max_pages, win,
+                                  tid == 0 && split == 0 && blockIdx.y == 0, status);
+  auto lim_of = [&](int r) { return max(0, min(len, len - n_q + 1 + (row0 + r) / G)); };
+  const int lim_lo = lim_of(0), lim_hi = lim_of(nh - 1);
+  const WinPages<true> wp(win, lim_lo, lim_hi);
+  const int p_begin = split * pages_per_split;   // slots of the pages to visit
+  const int n = min(wp.n_slots, p_begin + pages_per_split) - p_begin;
+  float* out_base = partials + ((size_t)s * n_q * n_q_heads) * n_splits * PS + (size_t)split * PS;
+  const size_t seq_row = (size_t)s * n_q * n_q_heads;
+  if (n <= 0) {  // empty: zero rows, or m = -inf, l = 0, acc = 0
+    if (out != nullptr) {
+      for (int i = tid; i < nh * D; i += kWThreads) {
+        const int r = row_index(i / D);
+        if (in_bounds(r < n_q * n_q_heads, status))
+          store_typed(out, (seq_row + r) * D + i % D, 0.f, win.out_dtype);
+      }
+    } else {
+      for (int i = tid; i < nh * PS; i += kWThreads) {
+        const int r = row_index(i / PS), c = i % PS;
+        if (in_bounds(r < n_q * n_q_heads, status))
+          out_base[(size_t)r * n_splits * PS + c] = c == D ? -CUDART_INF_F : 0.f;
+      }
+    }
+    return;
+  }
+  const int* pt_row = page_table + (size_t)s * max_pages;
+  auto phys_of = [&](int k) {
+    const int pg = wp.page(p_begin + k);
+    const int ph = in_bounds(pg < max_pages, status) ? __ldg(pt_row + pg) : -1;
+    return ph >= 0 && ph < n_pages ? ph : -1;
+  };
+
+  // ---- tensor memory, barriers, the first two pages ------------------------------------
+  if (warp == 12) tc::alloc(tmem_slot, kWCols);
+  auto issue = [&](int k) {  // one thread
+    const int st = k & 1, ph = phys_of(k);
+    if (ph >= 0) {
+      mbar_expect_tx(bars + kRing + st, BB);
+      bulk_copy(smem + SM::kOffRing + st * BB, blocks + ((size_t)ph * H + hk) * BB, BB, bars + kRing + st);
+    } else {
+      set_status(status, ISOQ_ST_PAGE_RANGE);
+      mbar_arrive(bars + kRing + st);  // complete the phase without data; the page is masked
+    }
+  };
+  if (tid == 256) {
+    for (int i = 0; i < kBars; ++i) {
+      const bool many = (i >= kKFull && i < kKFree) || (i >= kSRead && i < kPvDone);
+      mbar_init(bars + i, many ? 128 : 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    issue(0);
+    if (n > 1) issue(1);
+  }
+
+  // ---- a6: rotate the rows' queries into the A tiles (f16 high and low parts) ------------
+  if (warp < 12) {
+    float M[16];
+    load_block_mat(params + (size_t)hk * D * 4, lane, M);
+    const int k0 = lane * E;  // dims 4 lane .. + 3: half of one 16-byte core-matrix row
+    for (int r = warp; r < rows_cta; r += 12) {
+      float v[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = 0.f;
+      if (r < nh && in_bounds(row_index(r) < n_q * n_q_heads, status)) {
+        const TQ* qp = Q + (seq_row + row_index(r)) * D + k0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = to_f32<TQ>(qp[i]);
+      }
+      wht_warp<E>(v, lane);
+      float z[E], hi[E];
+      mat_fwd(M, v, z);
+#pragma unroll
+      for (int e = 0; e < E; ++e) hi[e] = __half2float(__float2half_rn(z[e]));
+      const uint32_t at = sQ + (r >> 7) * 65536 + (k0 >> 3) * 2048 + ((r & 127) >> 3) * 128 +
+                          (r & 7) * 16 + (k0 & 7) * 2;
+      if (!in_bounds(at + 32768 + 8 <= sK, status)) continue;
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(pack_f16x2(hi[0], hi[1])),
+                   "r"(pack_f16x2(hi[2], hi[3])) : "memory");
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 32768),
+                   "r"(pack_f16x2(z[0] - hi[0], z[1] - hi[1])),
+                   "r"(pack_f16x2(z[2] - hi[2], z[3] - hi[3])) : "memory");
+    }
+  }
+  fence_proxy_async();
+  tc::fence_before();
+  __syncthreads();  // barriers initialised, tensor memory allocated, query tiles written
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // jobs of softmax half w: page k = i with two row blocks, else k = 2 i + w
+  auto jobs = [&](int w) { return two ? n : (n - w + 1) / 2; };
+  bool ok = true;
+  // this thread's row state (softmax warps)
+  const int w = (warp >> 2) & 1, r_tid = tid & 127;
+  const int my_r = two ? 128 * w + r_tid : r_tid;
+  float m2 = -CUDART_INF_F, lsum = 0.f, sigma = 0.f;
+  const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+
+  if (warp >= 8 && warp < 12) {
+    // ================ dequantisation ======================================================
+    const int t = tid - 256;
+    uint32_t tl0, tl1, th0, th1;
+    level_tables<BITS>(tl0, tl1, th0, th1);
+    const float kf = scale * kLog2e / (ALPHA * (float)D);  // log2 score per (dot * nK)
+    int issued = min(n, 2), k = 0;
+    bool page_nx = phys_of(0) >= 0;  // looked up a page ahead
+    for (; k < n; ++k) {
+      const int st = k & 1;
+      const uint8_t* blk = smem + SM::kOffRing + st * BB;
+      ok = mbar_wait(bars + kRing + st, (k >> 1) & 1) &&
+           (k < 2 || mbar_wait(bars + kKFree + st, ((k - 2) >> 1) & 1));
+      if (ok) page_tile<BITS>(blk, 0, t, sK + st * kPageTile, tl0, tl1, th0, th1, status);
+      fence_proxy_async();  // the generic-proxy tile writes, before the tensor core reads
+      if (ok) mbar_arrive(bars + kKFull + st);
+      // the V tile, the norms and sigma of page k - 2 have been used once its value product is done
+      ok = ok && (k < 2 || mbar_wait(bars + kVFree + st, ((k - 2) >> 1) & 1));
+      // nrm[j] = |k_j| kf; nrm[64 + j] = |v_j| / sigma with the CTA's V-norm reference sigma (it
+      // only scales the weights), raised when a token some row sees has |v| > kSigmaSlack sigma
+      const int tok0 = wp.page(p_begin + k) * kPage;
+      const bool page_ok = page_nx;
+      if (k + 1 < n) page_nx = phys_of(k + 1) >= 0;
+      if (t < 64) {
+        if (ok) nrm[st * 128 + t] = half_at(blk + k_norm_off(D, BITS) + 2 * t) * kf;
+      } else {
+        const int j = t - 64;
+        float nv = half_at(blk + v_norm_off(D, BITS) + 2 * j);
+        nv = page_ok && tok0 + j < lim_hi && wp.any_sees(win, tok0 + j) ? nv : 0.f;
+        float pm = warp_max(nv);
+        if (lane == 0) red[warp - 10] = pm;
+        asm volatile("bar.sync 1, 64;" ::: "memory");  // warps 10 and 11
+        pm = fmaxf(red[0], red[1]);
+        sigma = pm > sigma * kSigmaSlack ? pm : sigma;
+        if (ok) {
+          nrm[st * 128 + t] = sigma > 0.f ? nv * (1.f / sigma) : 0.f;
+          if (t == 64) {
+            sig[st] = sigma;
+            valid[st] = page_ok;
+          }
+        }
+      }
+      if (ok) page_tile<BITS>(blk, 1, t, sV + st * kPageTile, tl0, tl1, th0, th1, status);
+      fence_proxy_async();
+      if (ok) mbar_arrive(bars + kVFull + st);
+      // the ring stage (and red) has been read; whether one of the 128 threads gave up
+      uint32_t gave_up;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, 128, p;\n"
+          " selp.u32 %0, 1, 0, q;\n}"
+          : "=r"(gave_up) : "r"((uint32_t)!ok) : "memory");
+      if (gave_up) break;
+      if (t == 0 && k + 2 < n) {
+        fence_proxy_async();
+        issue(k + 2);
+      }
+      if (k + 2 < n) issued = k + 3;
+    }
+    if (k < n) {  // gave up: wait (bounded) for the copies in flight
+      ok = false;
+      if (t == 0)
+        for (int kk = k; kk < issued; ++kk) mbar_wait(bars + kRing + (kk & 1), (kk >> 1) & 1);
+    }
+  } else if (warp == 12) {
+    // ================ products ============================================================
+    if (lane == 0) {
+      // a7: S_h(k), 8 k-steps of 16 dims, the high and the low part
+      auto scores = [&](int h, int k) {
+        const uint32_t q = sQ + (two ? h : 0) * 65536, kt = sK + (k & 1) * kPageTile;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t bd = tc::sdesc(kt + kk * 2048, 1024, 128);
+          tc::mma_ss(tmem + col_s(h), tc::sdesc(q + kk * 4096, 2048, 128), bd, kIdS, kk > 0);
+          tc::mma_ss(tmem + col_s(h), tc::sdesc(q + 32768 + kk * 4096, 2048, 128), bd, kIdS, 1);
+        }
+        tc::commit(bars + kSFull + h);
+      };
+      // a8: O_h += P'_h . V_hat(k), 4 k-steps of 16 tokens; i = the half's job number
+      auto values = [&](int h, int k, int i) {
+        const uint32_t vt = sV + (k & 1) * kPageTile;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          tc::mma_ts(tmem + col_o(h), tmem + col_p(h) + 8 * j, tc::sdesc(vt + j * 4096, 2048, 128),
+                     kIdO, (i > 0 || j > 0) ? 1u : 0u);
+        tc::commit(bars + kPvDone + h);
+      };
+      auto full = [&](int base, int k) { return mbar_wait(bars + base + (k & 1), (k >> 1) & 1); };
+      if (two) {
+        ok = full(kKFull, 0);
+        tc::fence_after();
+        if (ok) {
+          scores(0, 0);
+          scores(1, 0);
+          tc::commit(bars + kKFree);
+        }
+        for (int k = 0; ok && k < n; ++k) {
+          for (int h = 0; ok && h < 2; ++h) {
+            if (k + 1 < n) {  // the next page's scores as soon as this page's have been read
+              ok = (h || full(kKFull, k + 1)) && mbar_wait(bars + kSRead + h, k & 1);
+              if (!ok) break;
+              tc::fence_after();
+              scores(h, k + 1);
+              if (h) tc::commit(bars + kKFree + ((k + 1) & 1));
+            }
+            ok = (h || full(kVFull, k)) && mbar_wait(bars + kPFull + h, k & 1);
+            if (!ok) break;
+            tc::fence_after();
+            values(h, k, k);
+            if (h) tc::commit(bars + kVFree + (k & 1));
+          }
+        }
+      } else {
+        for (int k = 0; ok && k < 2 && k < n; ++k) {
+          ok = full(kKFull, k);
+          if (!ok) break;
+          tc::fence_after();
+          scores(k, k);
+          tc::commit(bars + kKFree + k);
+        }
+        for (int k = 0; ok && k < n; ++k) {
+          const int h = k & 1, i = k >> 1;
+          if (k + 2 < n) {
+            ok = full(kKFull, k + 2) && mbar_wait(bars + kSRead + h, i & 1);
+            if (!ok) break;
+            tc::fence_after();
+            scores(h, k + 2);
+            tc::commit(bars + kKFree + h);
+          }
+          ok = full(kVFull, k) && mbar_wait(bars + kPFull + h, i & 1);
+          if (!ok) break;
+          tc::fence_after();
+          values(h, k, i);
+          tc::commit(bars + kVFree + h);
+        }
+      }
+      if (!ok) {  // gave up: wait (bounded) for the products in flight
+        tc::commit(bars + kDrain);
+        mbar_wait(bars + kDrain, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ================ softmax of this thread's row ==========================================
+    const int my_lim = my_r < nh ? lim_of(my_r) : lim_hi;
+    const int my_lo = win_lo<true>(win, my_lim);
+    const uint32_t t_s = t_lane + col_s(w), t_p = t_lane + col_p(w), t_o = t_lane + col_o(w);
+    const int n_jobs = jobs(w);
+    for (int i = 0; i < n_jobs; ++i) {
+      const int k = two ? i : 2 * i + w, st = k & 1;
+      // the page's norms, then its scores (warp-uniform: collective loads follow)
+      ok = __all_sync(kFull, mbar_wait(bars + kVFull + st, (k >> 1) & 1) &&
+                                 mbar_wait(bars + kSFull + w, i & 1));
+      if (!ok) break;
+      tc::fence_after();
+      float x[64];
+      {
+        uint32_t sr[64];
+        tc::ld64(t_s, sr);
+#pragma unroll
+        for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(sr[j]);
+      }
+      tc::fence_before();
+      mbar_arrive(bars + kSRead + w);
+      const float* nk = nrm + st * 128;
+      const bool page_ok = valid[st] != 0;
+      const int tok0 = wp.page(p_begin + k) * kPage;
+      const float sg = sig[st];
+      const float vr = sg > sigma ? sigma / sg : 1.f;  // 0 on the first valid page
+      sigma = sg;
+      const bool all = page_ok && tok0 + kPage <= lim_lo && wp.page_full(win, tok0);
+      // exponents a_j = s_j |k_j| - m2 from one FMA each; m2 moves only when some a_j > kLazy (or
+      // on the row's first scores), and then O is rescaled in place, factor resc
+      float resc = vr;
+      bool moved = vr != 1.f;
+      auto exponents = [&](auto full_c) {
+        constexpr bool FULL = decltype(full_c)::value;
+        auto sees = [&](int tok) { return page_ok && tok < my_lim && win_sees<true>(win, my_lo, tok); };
+        const bool fresh = m2 == -CUDART_INF_F;
+        const float2 nm2 = fresh ? make_float2(0.f, 0.f) : make_float2(-m2, -m2);
+        float am[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (int j4 = 0; j4 < 64; j4 += 4) {
+          const float4 k4 = *reinterpret_cast<const float4*>(nk + j4);
+          const float2 a01 = f2_fma(make_float2(x[j4], x[j4 + 1]), make_float2(k4.x, k4.y), nm2);
+          const float2 a23 = f2_fma(make_float2(x[j4 + 2], x[j4 + 3]), make_float2(k4.z, k4.w), nm2);
+          const float av[4] = {a01.x, a01.y, a23.x, a23.y};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float a = av[e];
+            if constexpr (!FULL) a = sees(tok0 + j4 + e) ? a : -CUDART_INF_F;
+            x[j4 + e] = a;
+            am[e] = fmaxf(am[e], a);
+          }
+        }
+        const float amax = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
+        if (fresh ? amax != -CUDART_INF_F : amax > kLazy) {
+          const float f = fresh ? 0.f : ex2(-amax);  // fresh: nothing accumulated yet
+          resc *= f;
+          lsum *= f;
+          m2 = fresh ? amax : m2 + amax;
+          moved = true;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) x[j] -= amax;
+        }
+      };
+      if (all) exponents(std::true_type{});
+      else exponents(std::false_type{});
+      uint32_t pw[32];
+      float2 ls01 = make_float2(0.f, 0.f), ls23 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j4 = 0; j4 < 64; j4 += 4) {
+        const float4 v4 = *reinterpret_cast<const float4*>(nk + 64 + j4);
+        const float2 p01 = make_float2(ex2(x[j4]), ex2(x[j4 + 1]));  // -inf: 0
+        const float2 p23 = make_float2(ex2(x[j4 + 2]), ex2(x[j4 + 3]));
+        ls01 = f2_add(ls01, p01);
+        ls23 = f2_add(ls23, p23);
+        const float2 w01 = f2_mul(p01, make_float2(v4.x, v4.y));
+        const float2 w23 = f2_mul(p23, make_float2(v4.z, v4.w));
+        pw[j4 / 2] = pack_f16x2(w01.x, w01.y);
+        pw[j4 / 2 + 1] = pack_f16x2(w23.x, w23.y);
+      }
+      lsum += (ls01.x + ls01.y) + (ls23.x + ls23.y);
+      // P' and O are this thread's again once the half's last value product is done
+      ok = __all_sync(kFull, i == 0 || mbar_wait(bars + kPvDone + w, (i - 1) & 1));
+      if (!ok) break;
+      tc::fence_after();
+      if (i > 0 && __any_sync(kFull, moved)) {  // collective: the other rows with factor 1
+        uint32_t ov[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tc::ld32(t_o + 32 * c, ov);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * resc);
+          tc::st32(t_o + 32 * c, ov);
+        }
+      }
+      tc::st32(t_p, pw);
+      tc::wait_st();
+      tc::fence_before();
+      mbar_arrive(bars + kPFull + w);
+    }
+    if (ok && n_jobs > 0) ok = mbar_wait(bars + kPvDone + w, (n_jobs - 1) & 1);
+  }
+
+  // ---- every role is through: the rows' results ------------------------------------------
+  tc::fence_before();
+  const bool failed = __syncthreads_or(!ok);
+  tc::fence_after();
+  if (failed) {
+    if (tid == 0) set_status(status, ISOQ_ST_TIMEOUT);
+  } else {
+    const float f = sigma / ALPHA;  // O holds sum p |v| ALPHA L / sigma
+    const bool softmax = warp < 8;
+    float o[D];
+    if (softmax) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t ov[32];
+        tc::ld32(t_lane + col_o(w) + 32 * c, ov);
+        // a half without pages has no product: its columns hold nothing
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[32 * c + j] = jobs(w) > 0 ? __uint_as_float(ov[j]) * f : 0.f;
+      }
+    }
+    if (!two) {  // the halves' states of the same rows meet in the query tiles' memory
+      auto at = [&](int r, int c) { return smem + r * 512 + ((c ^ (r & 7)) << 4); };
+      if (softmax && w == 1) {
+        ml1[r_tid] = make_float2(m2, lsum);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          *reinterpret_cast<float4*>(at(r_tid, c)) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+      }
+      __syncthreads();
+      if (softmax && w == 0) {
+        const float2 b = ml1[r_tid];
+        const float M = fmaxf(m2, b.x);
+        const float fa = m2 == -CUDART_INF_F ? 0.f : ex2(m2 - M);
+        const float fb = b.x == -CUDART_INF_F ? 0.f : ex2(b.x - M);
+        m2 = M;
+        lsum = lsum * fa + b.y * fb;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(at(r_tid, c));
+          o[4 * c] = fmaf(v.x, fb, o[4 * c] * fa);
+          o[4 * c + 1] = fmaf(v.y, fb, o[4 * c + 1] * fa);
+          o[4 * c + 2] = fmaf(v.z, fb, o[4 * c + 2] * fa);
+          o[4 * c + 3] = fmaf(v.w, fb, o[4 * c + 3] * fa);
+        }
+      }
+    }
+    if (softmax && (two || w == 0) && my_r < nh) {
+      const int r = row_index(my_r);
+      if (in_bounds(r < n_q * n_q_heads, status)) {
+        if (out != nullptr) {
+          finish_row(o, params + (size_t)hk * D * 4, lsum > 0.f ? 1.f / (lsum * (float)D) : 0.f, out,
+                     (seq_row + r) * D, win.out_dtype);
+        } else {
+          float* p = out_base + (size_t)r * n_splits * PS;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            *reinterpret_cast<float4*>(p + 4 * c) =
+                make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          p[D] = m2 == -CUDART_INF_F ? -CUDART_INF_F : m2 / kLog2e;  // natural-log units
+          p[D + 1] = lsum;
+        }
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc::fence_after();
+    tc::dealloc(tmem, kWCols);
+  }
+}
+
+template <typename TQ, int BITS>
+cudaError_t launch_window_t(const DecodeArgs& a, cudaStream_t stream) {
+  using SM = WinSmem<BITS>;
+  static unsigned long long attr_set = 0;  // the shared-memory opt-in, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((attr_set >> dev) & 1ull)) {
+    e = cudaFuncSetAttribute(window_tc_kernel<TQ, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             SM::kBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set |= 1ull << dev;
+  }
+  const int rows = a.n_q * (a.n_q_heads / a.n_kv_heads), per = window_tc_rows(rows);
+  dim3 grid(a.n_splits, a.n_kv_heads * ((rows + per - 1) / per), a.n_seqs);
+  window_tc_kernel<TQ, BITS><<<grid, kWThreads, SM::kBytes, stream>>>(
+      a.params, a.blocks, a.page_table, a.n_pages, a.max_pages, a.n_kv_heads,
+      static_cast<const TQ*>(a.Q), a.n_q_heads, a.n_q, a.seq_lens, a.scale, a.pages_per_split,
+      a.n_splits, a.partials, a.n_splits == 1 ? a.out : nullptr, a.status, win_args(a));
+  return cudaGetLastError();
+}
+
+template <int BITS>
+cudaError_t launch_window_b(const DecodeArgs& a, cudaStream_t stream) {
+  switch (a.q_dtype) {
+    case ISOQ_F32: return launch_window_t<float, BITS>(a, stream);
+    case ISOQ_BF16: return launch_window_t<__nv_bfloat16, BITS>(a, stream);
+    case ISOQ_F16: return launch_window_t<__half, BITS>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_window_tc(const DecodeArgs& a, cudaStream_t stream) {
+  switch (a.bits) {
+    case 2: return launch_window_b<2>(a, stream);
+    case 3: return launch_window_b<3>(a, stream);
+    case 4: return launch_window_b<4>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace isoq

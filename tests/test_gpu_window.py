@@ -155,6 +155,16 @@ CHUNK = [
     dict(lens=[600, 300], hq=8, hkv=2, W=100, S=3, n_q=70, bits=2, out="f16"),
     dict(lens=[900, 130], hq=16, hkv=8, W=300, S=5, n_q=11, d=256),
     dict(lens=[4400], hq=8, hkv=1, W=3000, S=64, n_q=200),
+    # 36 .. 128 rows per KV head: two halves take the pages in turn (one page, two, odd and even)
+    dict(lens=[40, 64, 65, 128, 130, 200], hq=8, hkv=2, W=10 ** 6, S=0, n_q=9, out="f32"),
+    dict(lens=[3000, 61, 0, 2], hq=8, hkv=2, W=500, S=3, n_q=32, q="f16", out="f16"),
+    # 129 rows and more: two row blocks share the pages, the second one short or empty
+    dict(lens=[700, 64, 3], hq=3, hkv=3, W=300, S=5, n_q=129, out="f32"),
+    dict(lens=[700, 100], hq=16, hkv=2, W=130, S=64, n_q=33),
+    dict(lens=[2000, 320], hq=8, hkv=1, W=600, S=1, n_q=64, bits=4, q="f16", out="f16"),
+    dict(lens=[64], hq=16, hkv=1, W=7, S=0, n_q=64, bits=2),             # one page
+    dict(lens=[20000], hq=8, hkv=2, W=16000, S=4, n_q=10, out="f32"),    # chunks and the combine
+    dict(lens=[20000, 9000], hq=8, hkv=2, W=16000, S=4, n_q=70),
 ]
 
 
@@ -292,7 +302,8 @@ def test_window_refusals():
                      (dict(Q=None), iq.ISOQ_E_ARG), (dict(sl=None), iq.ISOQ_E_ARG), (dict(ws=None), iq.ISOQ_E_ARG),
                      (dict(L=-1), iq.ISOQ_E_ARG), (dict(n=2), iq.ISOQ_E_ARG), (dict(hq=7), iq.ISOQ_E_GQA),
                      (dict(hq=34), iq.ISOQ_E_GQA), (dict(nb=8), iq.ISOQ_E_WORKSPACE),
-                     (dict(ws=ws.data_ptr() + 4), iq.ISOQ_E_WORKSPACE), (dict(scale=float("nan")), iq.ISOQ_E_ARG)]:
+                     (dict(ws=ws.data_ptr() + 4), iq.ISOQ_E_WORKSPACE),
+                     (dict(out=out.data_ptr() + 8), iq.ISOQ_E_ARG), (dict(scale=float("nan")), iq.ISOQ_E_ARG)]:
         assert call(**kw) == want, kw
     torch.cuda.synchronize()
     assert bool((out == 3.0).all())
