@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(kFull, *tmem_slot, 0);
+  const int role = __shfl_sync(kFull, warp, 0);  // warp-uniform to the compiler as well
   load_words(0);
 
   const int row0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);  // tensor-memory lanes row0 ..
@@ -316,16 +317,18 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
       fail = true;
       break;
     }
-    if (tid == 0) {
+    if (role == 0) {
       tc::fence_after();
+      const uint64_t ad = tc::sdesc(sA, 2048, 128), bd = tc::sdesc(sB, 2048, 128);
+      if (tc::elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t ad = tc::sdesc(sA + kk * 4096, 2048, 128);
-        tc::mma_ss(tmem, ad, tc::sdesc(sB + kk * 4096, 2048, 128), kId, kk > 0);
-        if constexpr (LO)
-          tc::mma_ss(tmem, ad, tc::sdesc(sB + SM::kPart + kk * 4096, 2048, 128), kId, 1);
+        for (int kk = 0; kk < D / 16; ++kk) {  // descriptors count 16 bytes
+          tc::mma_ss(tmem, ad + kk * 256, bd + kk * 256, kId, kk > 0);
+          if constexpr (LO) tc::mma_ss(tmem, ad + kk * 256, bd + SM::kPart / 16 + kk * 256, kId, 1);
+        }
+        tc::commit(bars + 1);
       }
-      tc::commit(bars + 1);
+      __syncwarp();
     }
     pending = true;
     if constexpr (SM::kTable) {  // the table's rows of this tile, while the product runs

