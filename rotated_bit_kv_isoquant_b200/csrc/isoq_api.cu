@@ -196,16 +196,18 @@ SplitPlan plan_window(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_
   const int G = n_q_heads / n_kv_heads > 0 ? n_q_heads / n_kv_heads : 1;
   if (!isoq::use_window_tc(d, n_q, G))
     return plan_pages(n_seqs, n_q_heads, n_kv_heads, d, pages, n_q, true);
-  // The tensor-memory kernel runs one CTA per SM: the number of chunks with the smallest
-  // (rounds of CTAs) x (pages of a chunk + its start and end), in units of a page's time.  A
-  // start and end (128 or 256 queries rotated, the rows written) cost about 8 pages; more than
-  // one chunk adds the combine.
+  // The tensor-memory kernel runs one CTA per SM: the number of chunks with the smallest time
+  // in units of a page's (~2 us).  Rounds of CTAs, each the pages of a chunk plus a start and
+  // end (queries rotated, rows written) of about 12 pages; more than one chunk adds the combine:
+  // its launch, about 2 pages, and the partial rows written and read, ~6 MB in a page's time.
   const int per = isoq::window_tc_rows(n_q * G), slots = sm_count();
   const long long units = (long long)n_seqs * n_kv_heads * (((long long)n_q * G + per - 1) / per);
+  const double part_mb = 2e-6 * n_seqs * (double)n_q * n_q_heads * isoq::partial_stride(d) * 4;
   int best = 1;
-  long long best_cost = -1;
+  double best_cost = -1;
   for (int s = 1; s <= pages && s <= 64; ++s) {
-    const long long cost = ((units * s + slots - 1) / slots) * ((pages + s - 1) / s + 8) + (s > 1 ? 4 : 0);
+    const double cost = (double)((units * s + slots - 1) / slots) * ((pages + s - 1) / s + 12) +
+                        (s > 1 ? 2 + s * part_mb / 6 : 0);
     if (best_cost < 0 || cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -677,7 +679,8 @@ int window_common(const isoq_params* params, const isoq_cache* cache, const void
                   size_t workspace_bytes, void* stream) {
   if (window < 1 || n_sinks < 0 || !valid_dtype(out_dtype)) return ISOQ_E_ARG;
   if (!out && n_seqs > 0 && n_q_heads > 0) return ISOQ_E_ARG;
-  if (((uintptr_t)out & 15u) != 0) return ISOQ_E_ARG;  // rows are written in 16-byte pieces
+  // rows are read and written in 16-byte pieces
+  if (((uintptr_t)out & 15u) != 0 || ((uintptr_t)Q & 15u) != 0) return ISOQ_E_ARG;
   return decode_common_impl(params, cache, Q, q_dtype, n_seqs, n_q, n_q_heads, seq_lens,
                             max_seq_len, window, n_sinks, out, out_dtype, nullptr, scale, workspace,
                             workspace_bytes, stream);

@@ -19,8 +19,8 @@
 //
 // The score queries keep an f16 high and low part, the weights P' are f16 with f32
 // accumulators, statistics are f32 (as in the multi-token kernel, whose error bounds hold).
-// A call whose rows' pages fit one chunk divides, rotates back and writes its output here: a
-// thread holds its whole row.  Otherwise partial states go to the combine.
+// A call whose rows' pages fit one chunk divides, rotates back and writes its output here.
+// Otherwise partial states go to the combine.
 #include <math_constants.h>
 
 #include <type_traits>
@@ -62,58 +62,27 @@ struct WinSmem {
   static constexpr int kOffNorm = kOffRing + 2 * kBB;   // float [2][64 K | 64 V]
   static constexpr int kOffMeta = kOffNorm + 2 * 128 * 4;  // float [2] sigma, int [2] page is valid
   static constexpr int kOffRed = kOffMeta + 16;         // float [2]
-  static constexpr int kOffMl = kOffRed + 16;           // float2 [128]: m, l of the second half
-  static constexpr int kOffBar = kOffMl + 128 * 8;
+  static constexpr int kOffMl = kOffRed + 16;           // float2 [2 halves][128]: m, l
+  static constexpr int kOffRow = kOffMl + 256 * 8;      // int [256]: output row of each row
+  static constexpr int kOffBar = kOffRow + 256 * 4;
   static constexpr int kOffTmem = kOffBar + kBars * 8 + 8;
   static constexpr int kBytes = kOffTmem + 16;
   static_assert(kOffRing % 16 == 0 && kBB % 16 == 0 && kOffBar % 8 == 0 && kOffNorm % 16 == 0, "");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-// One row of 128 rotated values: inverse blocks, WHT, factor; written in the caller's type.
-__device__ __forceinline__ void finish_row(float (&o)[kWD], const float* __restrict__ head_mats,
-                                           float factor, void* out, size_t at, int dtype) {
+// wht_warp of a 128-dim vector with the lanes' signs at hand: one multiply-add per element and
+// cross-lane stage (exact: a product with +-1), where many rows pass through.
+__device__ __forceinline__ void wht_signed(float (&v)[4], const float (&sgn)[5]) {
+  const float a = v[0] + v[1], b = v[0] - v[1], c = v[2] + v[3], d = v[2] - v[3];
+  v[0] = a + c;
+  v[1] = b + d;
+  v[2] = a - c;
+  v[3] = b - d;
 #pragma unroll
-  for (int b = 0; b < kWD / 4; ++b) {
-    float M[16], y[4];
-    load_block_mat(head_mats, b, M);
-    mat_inv(M, o + 4 * b, y);
+  for (int s = 0; s < 5; ++s)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[4 * b + i] = y[i] * factor;
-  }
-#pragma unroll
-  for (int h = 1; h < kWD; h <<= 1)
-#pragma unroll
-    for (int i = 0; i < kWD; i += 2 * h)
-#pragma unroll
-      for (int j = i; j < i + h; ++j) {
-        const float a = o[j], b = o[j + h];
-        o[j] = a + b;
-        o[j + h] = a - b;
-      }
-  if (dtype == ISOQ_F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-    for (int i = 0; i < kWD / 4; ++i)
-      p[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-    return;
-  }
-  uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
-#pragma unroll
-  for (int i = 0; i < kWD / 8; ++i) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float a = o[8 * i + 2 * e], b = o[8 * i + 2 * e + 1];
-      if (dtype == ISOQ_F16) {
-        w[e] = pack_f16x2(a, b);
-      } else {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        w[e] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-    }
-    p[i] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+    for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], sgn[s], __shfl_xor_sync(kFull, v[j], 1 << s));
 }
 
 template <typename TQ, int BITS>
@@ -135,7 +104,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
   float* sig = reinterpret_cast<float*>(smem + SM::kOffMeta);
   int* valid = reinterpret_cast<int*>(smem + SM::kOffMeta) + 2;
   float* red = reinterpret_cast<float*>(smem + SM::kOffRed);
-  float2* ml1 = reinterpret_cast<float2*>(smem + SM::kOffMl);
+  float2* ml = reinterpret_cast<float2*>(smem + SM::kOffMl);
+  int* row_off = reinterpret_cast<int*>(smem + SM::kOffRow);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kOffTmem);
   const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + SM::kOffK), sV = smem_u32(smem + SM::kOffV);
 
@@ -207,35 +177,48 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (n > 1) issue(1);
   }
 
+  if (tid < 256) row_off[tid] = tid < nh ? row_index(tid) : n_q * n_q_heads;
+  float sgn[5];  // the lane's side of each cross-lane stage of the WHT
+#pragma unroll
+  for (int i = 0; i < 5; ++i) sgn[i] = ((lane >> i) & 1) ? -1.f : 1.f;
+  __syncthreads();  // the rows' places
   // ---- a6: rotate the rows' queries into the A tiles (f16 high and low parts) ------------
   if (warp < 12) {
     float M[16];
     load_block_mat(params + (size_t)hk * D * 4, lane, M);
     const int k0 = lane * E;  // dims 4 lane .. + 3: half of one 16-byte core-matrix row
-    for (int r0 = warp; r0 < rows_cta; r0 += 12 * 4) {  // four rows' loads and shuffles at a time
-      float v[4][E];
+    constexpr int kAt = 4;  // rows at a time; the next four's loads run meanwhile
+    auto load = [&](int r0, float (&v)[kAt][E]) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kAt; ++j) {
         const int r = r0 + 12 * j;
 #pragma unroll
         for (int i = 0; i < E; ++i) v[j][i] = 0.f;
-        if (r < nh && in_bounds(row_index(r) < n_q * n_q_heads, status)) {
-          const TQ* qp = Q + (seq_row + row_index(r)) * D + k0;
-#pragma unroll
-          for (int i = 0; i < E; ++i) v[j][i] = to_f32<TQ>(qp[i]);
-        }
+        if (r < nh && in_bounds(row_off[r] < n_q * n_q_heads, status))
+          load_vec<TQ, E>(Q + (seq_row + row_off[r]) * D + k0, v[j]);
       }
+    };
+    float nx[kAt][E];
+    load(warp, nx);
+#pragma unroll 1
+    for (int r0 = warp; r0 < rows_cta; r0 += 12 * kAt) {
+      float v[kAt][E];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) wht_warp<E>(v[j], lane);
+      for (int j = 0; j < kAt; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+        for (int i = 0; i < E; ++i) v[j][i] = nx[j][i];
+      load(r0 + 12 * kAt, nx);
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) wht_signed(v[j], sgn);
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
         const int r = r0 + 12 * j;
         float z[E], hi[E];
         mat_fwd(M, v[j], z);
 #pragma unroll
         for (int e = 0; e < E; ++e) hi[e] = __half2float(__float2half_rn(z[e]));
-        const uint32_t at = sQ + (r >> 7) * 2 * SM::kQPart + (k0 >> 3) * SM::kQGroup + ((r & 127) >> 3) * 128 +
-                            (r & 7) * 16 + (k0 & 7) * 2;
+        const uint32_t at = sQ + (r >> 7) * 2 * SM::kQPart + (k0 >> 3) * SM::kQGroup +
+                            ((r & 127) >> 3) * 128 + (r & 7) * 16 + (k0 & 7) * 2;
         if (r >= rows_cta || !in_bounds(at + SM::kQPart + 8 <= sK, status)) continue;
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(pack_f16x2(hi[0], hi[1])),
                      "r"(pack_f16x2(hi[2], hi[3])) : "memory");
@@ -514,59 +497,92 @@ __global__ void __launch_bounds__(kWThreads, 1)
   if (failed) {
     if (tid == 0) set_status(status, ISOQ_ST_TIMEOUT);
   } else {
-    const float f = sigma / ALPHA;  // O holds sum p |v| ALPHA L / sigma
-    const bool softmax = warp < 8;
-    float o[D];
-    if (softmax) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+    // The rows' accumulators go through the query tiles' memory, one 512-byte row of 32 chunks
+    // each (chunk index xor the row's low bits), and a warp finishes a row: rolled loops, since
+    // straight-line code that runs once per CTA costs its fetches (a register-resident inverse
+    // rotation, one thread a row, took 80 us a CTA).
+    auto at = [&](int r, int c) { return reinterpret_cast<float4*>(smem + r * 512 + ((c ^ (r & 7)) << 4)); };
+    if (role < 8) {
+      const float f = jobs(w) > 0 ? sigma / ALPHA : 0.f;  // O holds sum p |v| ALPHA L / sigma
+      const int r = 128 * w + r_tid;
+      ml[r] = make_float2(m2, lsum);
+#pragma unroll 1
+      for (int c = 0; c < 4 && jobs(w) > 0; ++c) {
         uint32_t ov[32];
         tc::ld32(t_lane + col_o(w) + 32 * c, ov);
-        // a half without pages has no product: its columns hold nothing
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[32 * c + j] = jobs(w) > 0 ? __uint_as_float(ov[j]) * f : 0.f;
+        for (int j = 0; j < 8; ++j)
+          *at(r, 8 * c + j) =
+              make_float4(__uint_as_float(ov[4 * j]) * f, __uint_as_float(ov[4 * j + 1]) * f,
+                          __uint_as_float(ov[4 * j + 2]) * f, __uint_as_float(ov[4 * j + 3]) * f);
       }
     }
-    if (!two) {  // the halves' states of the same rows meet in the query tiles' memory
-      auto at = [&](int r, int c) { return smem + r * 512 + ((c ^ (r & 7)) << 4); };
-      if (softmax && w == 1) {
-        ml1[r_tid] = make_float2(m2, lsum);
+    __syncthreads();
+    if (role < 12) {
+      float M[16];
+      load_block_mat(params + (size_t)hk * D * 4, lane, M);
+      constexpr int kAt = 4;  // rows at a time
+#pragma unroll 1
+      for (int r0 = role; r0 < nh; r0 += 12 * kAt) {
+        float y[kAt][E], m[kAt], l[kAt];
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          *reinterpret_cast<float4*>(at(r_tid, c)) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-      }
-      __syncthreads();
-      if (softmax && w == 0) {
-        const float2 b = ml1[r_tid];
-        const float M = fmaxf(m2, b.x);
-        const float fa = m2 == -CUDART_INF_F ? 0.f : ex2(m2 - M);
-        const float fb = b.x == -CUDART_INF_F ? 0.f : ex2(b.x - M);
-        m2 = M;
-        lsum = lsum * fa + b.y * fb;
+        for (int j = 0; j < kAt; ++j) {
+          const int r = min(r0 + 12 * j, nh - 1);
+          const float2 a = ml[r];
+          const float4 v = *at(r, lane);
+          m[j] = a.x;
+          float fa = 1.f, fb = 0.f;
+          float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+          l[j] = a.y;
+          if (!two && jobs(1) > 0) {  // the halves' states of the same row meet
+            const float2 b = ml[128 + r];
+            u = *at(128 + r, lane);
+            m[j] = fmaxf(a.x, b.x);
+            fa = a.x == -CUDART_INF_F ? 0.f : ex2(a.x - m[j]);
+            fb = b.x == -CUDART_INF_F ? 0.f : ex2(b.x - m[j]);
+            l[j] = a.y * fa + b.y * fb;
+          }
+          const float o[E] = {fmaf(u.x, fb, v.x * fa), fmaf(u.y, fb, v.y * fa), fmaf(u.z, fb, v.z * fa),
+                              fmaf(u.w, fb, v.w * fa)};
+          if (out != nullptr) {
+            mat_inv(M, o, y[j]);
+          } else {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float4 v = *reinterpret_cast<const float4*>(at(r_tid, c));
-          o[4 * c] = fmaf(v.x, fb, o[4 * c] * fa);
-          o[4 * c + 1] = fmaf(v.y, fb, o[4 * c + 1] * fa);
-          o[4 * c + 2] = fmaf(v.z, fb, o[4 * c + 2] * fa);
-          o[4 * c + 3] = fmaf(v.w, fb, o[4 * c + 3] * fa);
+            for (int i = 0; i < E; ++i) y[j][i] = o[i];
+          }
         }
-      }
-    }
-    if (softmax && (two || w == 0) && my_r < nh) {
-      const int r = row_index(my_r);
-      if (in_bounds(r < n_q * n_q_heads, status)) {
         if (out != nullptr) {
-          finish_row(o, params + (size_t)hk * D * 4, lsum > 0.f ? 1.f / (lsum * (float)D) : 0.f, out,
-                     (seq_row + r) * D, win.out_dtype);
-        } else {
-          float* p = out_base + (size_t)r * n_splits * PS;
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            *reinterpret_cast<float4*>(p + 4 * c) =
-                make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-          p[D] = m2 == -CUDART_INF_F ? -CUDART_INF_F : m2 / kLog2e;  // natural-log units
-          p[D + 1] = lsum;
+          for (int j = 0; j < kAt; ++j) wht_signed(y[j], sgn);
+        }
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) {
+          const int r = r0 + 12 * j;
+          if (r >= nh) continue;
+          const int ri = row_off[r];
+          if (!in_bounds(ri < n_q * n_q_heads, status)) continue;
+          if (out != nullptr) {  // divided by l, the WHT's and the levels' 1 / sqrt(d) each
+            const float f = l[j] > 0.f ? 1.f / (l[j] * (float)D) : 0.f;
+            const size_t at0 = (seq_row + ri) * D + lane * E;
+            const float4 v = make_float4(y[j][0] * f, y[j][1] * f, y[j][2] * f, y[j][3] * f);
+            if (win.out_dtype == ISOQ_F32) {
+              *reinterpret_cast<float4*>(static_cast<float*>(out) + at0) = v;
+            } else if (win.out_dtype == ISOQ_F16) {
+              *reinterpret_cast<uint2*>(static_cast<__half*>(out) + at0) =
+                  make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
+            } else {
+              __nv_bfloat162* p = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(out) + at0);
+              p[0] = __floats2bfloat162_rn(v.x, v.y);
+              p[1] = __floats2bfloat162_rn(v.z, v.w);
+            }
+          } else {
+            float* p = out_base + (size_t)ri * n_splits * PS;
+            *reinterpret_cast<float4*>(p + lane * E) = make_float4(y[j][0], y[j][1], y[j][2], y[j][3]);
+            if (lane == 0) {
+              p[D] = m[j] == -CUDART_INF_F ? -CUDART_INF_F : m[j] / kLog2e;  // natural-log units
+              p[D + 1] = l[j];
+            }
+          }
         }
       }
     }

@@ -303,7 +303,7 @@ def test_window_refusals():
                      (dict(L=-1), iq.ISOQ_E_ARG), (dict(n=2), iq.ISOQ_E_ARG), (dict(hq=7), iq.ISOQ_E_GQA),
                      (dict(hq=34), iq.ISOQ_E_GQA), (dict(nb=8), iq.ISOQ_E_WORKSPACE),
                      (dict(ws=ws.data_ptr() + 4), iq.ISOQ_E_WORKSPACE),
-                     (dict(out=out.data_ptr() + 8), iq.ISOQ_E_ARG), (dict(scale=float("nan")), iq.ISOQ_E_ARG)]:
+                     (dict(out=out.data_ptr() + 8), iq.ISOQ_E_ARG), (dict(Q=Q.data_ptr() + 2), iq.ISOQ_E_ARG), (dict(scale=float("nan")), iq.ISOQ_E_ARG)]:
         assert call(**kw) == want, kw
     torch.cuda.synchronize()
     assert bool((out == 3.0).all())
