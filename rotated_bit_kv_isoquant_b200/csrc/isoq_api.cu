@@ -121,6 +121,8 @@ int sm_count() {
 struct SplitPlan {
   int n_splits;
   int pages_per_split;
+  bool in_cluster = false;  // windowed row-block kernels: the chunks are one cluster's CTAs
+  bool wide = false;        // ... of 16 (d = 128) or 8 warps instead of 4
 };
 
 #ifndef ISOQ_DEC_WAVES
@@ -139,17 +141,23 @@ struct SplitPlan {
 // Context chunking for the decode kernel: about ISOQ_DEC_WAVES waves of (chunk, KV head,
 // query-head block, sequence) CTAs at the kernel's resident CTAs per SM, each chunk a whole
 // number of pages and at least min_pages pages when the context allows.
-SplitPlan plan_pages(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_pages, int n_q,
-                     bool windowed) {
+// Pages of a context of at most len tokens (at least one, so that a plan has a chunk).
+int pages_of(int len) {
+  return len > 0 ? (int)(((long long)len + ISOQ_PAGE_SIZE - 1) / ISOQ_PAGE_SIZE) : 1;
+}
+
+SplitPlan plan_splits(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_seq_len,
+                      int n_q = 1) {
   const int group = n_kv_heads > 0 ? n_q_heads / n_kv_heads : 1;
   // the multi-token kernels (64 or 128 rows per CTA, 2 CTAs per SM) when a chunk gives a
   // KV head at least 16 rows; else the per-row kernel (8 rows per CTA)
-  const bool shared_mq = d == 128 && n_q > 1 && (long long)n_q * group >= 16 && !windowed;
+  const bool shared_mq = d == 128 && n_q > 1 && (long long)n_q * group >= 16;
   const int n_sm = sm_count() * (shared_mq ? 2 : isoq::decode_i8_resident_ctas(d));
   const int rows_per_cta = shared_mq ? isoq::attention_rows_per_cta(d, n_q, group)
                                      : isoq::decode_rows_per_block(d, n_q, group);
   // pages per CTA worth a launch: the tensor-memory kernel rotates 128 queries per CTA
   const int min_pages = shared_mq ? (rows_per_cta == 128 ? 16 : 4) : ISOQ_DEC_MIN_PAGES;
+  const int max_pages = pages_of(max_seq_len);
   const long long units =
       (long long)n_seqs * n_kv_heads * (((long long)n_q * group + rows_per_cta - 1) / rows_per_cta);
   const long long target = (long long)n_sm * (shared_mq ? ISOQ_MQ_WAVES : ISOQ_DEC_WAVES);
@@ -163,16 +171,6 @@ SplitPlan plan_pages(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_p
   if (pps > isoq::kMaxPagesPerSplit) pps = isoq::kMaxPagesPerSplit;
   int n_splits = (max_pages + pps - 1) / pps;
   return SplitPlan{n_splits, pps};
-}
-
-// Pages of a context of at most len tokens (at least one, so that a plan has a chunk).
-int pages_of(int len) {
-  return len > 0 ? (int)(((long long)len + ISOQ_PAGE_SIZE - 1) / ISOQ_PAGE_SIZE) : 1;
-}
-
-SplitPlan plan_splits(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_seq_len,
-                      int n_q = 1) {
-  return plan_pages(n_seqs, n_q_heads, n_kv_heads, d, pages_of(max_seq_len), n_q, false);
 }
 
 // Most pages that the rows of one CTA can see with a window of W tokens and S sinks: a CTA
@@ -190,12 +188,66 @@ int window_pages(int n_q_heads, int n_kv_heads, int d, int max_seq_len, int n_q,
   return pages < all ? (int)pages : all;
 }
 
+// Chunks of the windowed row-block kernels: units (sequence, KV head, row block) of `pages`
+// pages, in one of three forms:
+//   wide CTAs, one per SM, up to 8 to a unit as a cluster (half a page a step and warp)
+//   4-warp CTAs, as many per SM as fit, up to 8 to a unit as a cluster
+//   4-warp CTAs with partial results in the workspace and the combine, any number to a unit
+// The one with the smallest estimated time is taken.  The estimate, in us, fitted to sweeps of
+// all three over 1 to 64 sequences, windows of 512 to 131072 tokens and d = 128 and 256 (within
+// 15% of most): a start of 2.5, a CTA's rotation and merge of 6.5, a page's step of one warp of
+// 1.75 alone to 4.75 with every warp of the SM busy, 0.3 for the cluster's exchange, 1.2 for the
+// combine, waves of CTAs one after another.  E.g. (wide, 4-warp cluster, partials; best of
+// each): 1 sequence x 4 KV heads x 17 pages 9.3, 9.4, 10.1; 8 x 8 x 66 20.1, 21.5, 22.3;
+// 64 x 8 x 129 192, 155, 157; 1 x 8 x 2048 91, 129, 48.
+SplitPlan plan_row_blocks(long long units, int d, int pages) {
+  const int sms = sm_count(), per_sm = isoq::decode_i8_resident_ctas(d);
+  const int narrow = sms * per_sm, warps = isoq::wide_warps(d);
+  SplitPlan best{1, pages, true, false};
+  double best_us = -1;
+  auto page_us = [](double busy) { return 1.75 + 3.0 * (busy < 1 ? busy : 1); };
+  auto offer = [&](int parts, bool in_cluster, bool wide) {
+    const int pps = (pages + parts - 1) / parts;
+    parts = (pages + pps - 1) / pps;
+    const double ctas = (double)units * parts;
+    double us = 2.5 + (in_cluster ? (parts > 1 ? 0.3 : 0) : 1.2);
+    if (wide) {
+      // one CTA takes an SM, and a cluster lies within one of the GPCs of 16 to 18 SMs: sizes
+      // that divide them, with room for what 4 and 8 leave over
+      if ((parts & (parts - 1)) != 0 || ctas > (parts <= 2 ? sms : sms - sms / 8)) return;
+      us += 6.5 + 0.5 * ((2 * pps + warps - 1) / warps) * page_us(2.0 * pps / warps);
+    } else {
+      const int steps = (pps + 3) / 4;
+      const double full = floor(ctas / narrow), rest = ctas - full * narrow;
+      us += full * (6.5 + steps * page_us(1));
+      if (rest > 0) us += 6.5 + steps * page_us(ceil(rest / sms) / per_sm);
+    }
+    if (pps <= isoq::kMaxPagesPerSplit && (best_us < 0 || us < best_us)) {
+      best_us = us;
+      best = SplitPlan{parts, pps, in_cluster, wide};
+    }
+  };
+  for (int parts = 1; parts <= pages && parts <= 8; ++parts) {
+    offer(parts, true, true);
+    offer(parts, true, false);
+  }
+  for (int parts = 9; parts <= pages && parts <= 128; ++parts) offer(parts, false, false);
+  if (best_us < 0) {  // contexts beyond 128 chunks of kMaxPagesPerSplit pages
+    const int pps = isoq::kMaxPagesPerSplit;
+    best = SplitPlan{(pages + pps - 1) / pps, pps, false, false};
+  }
+  return best;
+}
+
 SplitPlan plan_window(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_seq_len, int n_q,
                       int window, int n_sinks) {
   const int pages = window_pages(n_q_heads, n_kv_heads, d, max_seq_len, n_q, window, n_sinks);
   const int G = n_q_heads / n_kv_heads > 0 ? n_q_heads / n_kv_heads : 1;
-  if (!isoq::use_window_tc(d, n_q, G))
-    return plan_pages(n_seqs, n_q_heads, n_kv_heads, d, pages, n_q, true);
+  if (!isoq::use_window_tc(d, n_q, G)) {
+    const int RB = isoq::decode_rows_per_block(d, n_q, G);
+    return plan_row_blocks((long long)n_seqs * n_kv_heads * (((long long)n_q * G + RB - 1) / RB), d,
+                           pages);
+  }
   // The tensor-memory kernel runs one CTA per SM: the number of chunks with the smallest time
   // in units of a page's (~2 us).  Rounds of CTAs, each the pages of a chunk plus a start and
   // end (queries rotated, rows written) of about 12 pages; more than one chunk adds the combine:
@@ -643,6 +695,8 @@ int decode_common_impl(const isoq_params* params, const isoq_cache* cache, const
   a.window = window;
   a.n_sinks = n_sinks;
   a.max_len = max_seq_len;
+  a.in_cluster = plan.in_cluster;
+  a.wide = plan.wide;
   a.state = state;
   a.status = cache->status;
   cudaError_t e = isoq::launch_decode(a, (cudaStream_t)stream);

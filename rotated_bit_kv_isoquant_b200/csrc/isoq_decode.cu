@@ -180,7 +180,7 @@ static cudaError_t launch_dq(const DecodeArgs& a, cudaStream_t stream) {
                   : a.window == 0 && use_shared_mq(a) ? launch_decode_split_mq(a, stream)
                   : a.bits == 3                      ? launch_decode_split_i8(a, stream, &combined)
                                                      : launch_decode_split_mma(a, stream);
-  if (window_tc) combined = a.n_splits == 1;
+  if (a.window > 0) combined = window_tc ? a.n_splits == 1 : a.in_cluster;
   if (e != cudaSuccess) return e;
   if (combined) return cudaSuccess;
   const int rows = a.n_q * a.n_q_heads;

@@ -46,6 +46,7 @@
 
 #include "isoq_check.cuh"
 #include "isoq_common.cuh"
+#include "isoq_finish.cuh"
 #include "isoq_internal.h"
 #include "isoq_ptx.cuh"
 #include "isoq_vtile.cuh"
@@ -159,7 +160,7 @@ struct I8Smem {
   static constexpr int kRowOff = kKfOff + 8 * 4;                      // int [8]
   static constexpr int kBytes = kRowOff + 8 * 4;
   // the warps' states [NW][8][D + 4] and, for a single chunk, the merged rows [8][D + 1]
-  static constexpr int kMergeBytes = NW * 8 * (D + 4) * 4 + 8 * (D + 1) * 4;
+  static constexpr int kMergeBytes = NW * 8 * (D + 4) * 4 + 8 * (D + 4) * 4;
   static_assert(kMergeBytes <= kRing, "merge buffer must fit in the ring");
   static_assert(kAOff % 16 == 0 && kA2Off % 16 == 0, "A fragments must be aligned");
 };
@@ -194,7 +195,10 @@ constexpr int i8_min_blocks(int nw) {
 // rows, so it finishes the combine itself -- normalise, inverse rotation -- and writes the
 // output rows [n_seqs][n_q_heads][D] instead of partials.
 // WIN: sliding-window attention with sinks (isoq_window.cuh): the chunks are runs of the
-// pages that the rows can see, and out has the element type win.out_dtype.
+// pages that the rows can see, and out has the element type win.out_dtype.  With out and
+// several chunks, the chunks are the CTAs of a cluster (isoq_finish.cuh).  The wide CTAs of small
+// windowed grids hand a warp half a page (32 tokens) at a time, so that a window of a few pages
+// occupies all their warps: 17 pages on 4 CTAs of 16 warps are then one step a warp.
 template <int D, int NST, int RB, typename TQ, bool MQ, int NW, bool WIN>
 __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
     decode_i8_kernel(const float* __restrict__ params, const uint8_t* __restrict__ blocks,
@@ -211,6 +215,7 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
   constexpr int NG = D / 128;         // 32-dim groups per lane and token (groups t, t + 4)
   constexpr int NU = D / 128;         // unit pairs per lane in the V tile (g, g + 8)
   constexpr int MT = 8 * NU;          // m-tiles of the value product
+  constexpr int SUB = WIN && NW != 4 ? 2 : 1;  // tasks of a page
   constexpr int PS = D + 4;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
@@ -257,13 +262,14 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
   [[maybe_unused]] const size_t out_off0 = out_base - partials;
   if (tid < RB) row_off[tid] = tid < nh ? row_index(tid) : 0;
   __syncthreads();
-  // extent of the direct output (single chunk): [gridDim.z][n_q_heads][D]
-  [[maybe_unused]] const size_t out_len = (size_t)gridDim.z * n_q_heads * D;
-  if (p_begin >= p_end) {  // empty chunk: m = -inf, l = 0, acc = 0
+  // extent of the direct output (single chunk): [gridDim.z][n_q][n_q_heads][D]
+  [[maybe_unused]] const size_t out_len = (size_t)gridDim.z * n_q * n_q_heads * D;
+  const bool in_cluster = WIN && out != nullptr && n_splits > 1;
+  if (p_begin >= p_end && !in_cluster) {  // empty chunk: m = -inf, l = 0, acc = 0
     if (out != nullptr) {  // the whole context is empty: zero output rows
       for (int i = tid; i < nh * D; i += blockDim.x) {
         const int h = i / D, c = i - h * D;
-        const size_t o = ((size_t)s * n_q_heads + row_off[h]) * D + c;
+        const size_t o = ((size_t)s * n_q * n_q_heads + row_off[h]) * D + c;
         if (!in_bounds(o < out_len, status)) continue;
         if constexpr (WIN) store_typed(out, o, 0.f, win.out_dtype);
         else static_cast<float*>(out)[o] = 0.f;
@@ -288,15 +294,28 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
   }
   __syncwarp();
   const int* pt_row = page_table + (size_t)s * max_pages;
-  // page k of this warp: slot p_begin + warp + NW * k
-  const int n_my = (p_end - p_begin - warp + NW - 1) / NW;  // may be <= 0
+  // task k of this warp: page slot p_begin + (warp + NW * k) / SUB, its SUB-th part
+  const int n_my = (SUB * (p_end - p_begin) - warp + NW - 1) / NW;  // may be <= 0
   auto issue = [&](int k) {  // lane 0 only
-    const int pg = wp.page(p_begin + warp + NW * k);
+    const int pg = wp.page(p_begin + (warp + NW * k) / SUB);
     const int st = k % NST;
     const int phys = in_bounds(pg < max_pages && st < NST, status) ? __ldg(pt_row + pg) : -1;
     if (phys >= 0 && phys < n_pages && in_bounds(hk < H, status)) {
-      mbar_expect_tx(mybar + st, BB);
-      bulk_copy(myring + st * BB, blocks + ((size_t)phys * H + hk) * BB, BB, mybar + st);
+      const uint8_t* src = blocks + ((size_t)phys * H + hk) * BB;
+      uint8_t* dst = myring + st * BB;
+      mbar_expect_tx(mybar + st, BB / SUB);
+      if constexpr (SUB == 1) {
+        bulk_copy(dst, src, BB, mybar + st);
+      } else {  // 32 tokens' K codes, K norms, V codes and V norms, at their places in the block
+        const int part = (warp + NW * k) % SUB;
+        auto piece = [&](int off, int bytes) {
+          bulk_copy(dst + off + part * bytes, src + off + part * bytes, bytes, mybar + st);
+        };
+        piece(0, kPage * CB / SUB);
+        piece(k_norm_off(D, 3), 2 * kPage / SUB);
+        piece(v_codes_off(D, 3), kPage * CB / SUB);
+        piece(v_norm_off(D, 3), 2 * kPage / SUB);
+      }
     } else {
       set_status(status, ISOQ_ST_PAGE_RANGE);
       mbar_arrive(mybar + st);  // complete the phase without data; tokens are masked
@@ -419,7 +438,7 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
       break;
     }
     const uint8_t* blk = myring + st * BB;
-    const int pg = wp.page(p_begin + warp + NW * k);
+    const int pg = wp.page(p_begin + (warp + NW * k) / SUB);
     const int phys = in_bounds(pg < max_pages && st < NST, status) ? __ldg(pt_row + pg) : -1;
     const bool page_ok = phys >= 0 && phys < n_pages;
     const int tok0 = pg * kPage;
@@ -622,8 +641,14 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
         }
       }
     };
+    if constexpr (SUB == 1) {
 #pragma unroll
-    for (int tb = 0; tb < kPage; tb += 32) {
+      for (int tb = 0; tb < kPage; tb += 32) {
+        if (full) tile(tb, std::true_type{});
+        else tile(tb, std::false_type{});
+      }
+    } else {
+      const int tb = (warp + NW * k) % SUB * 32;
       if (full) tile(tb, std::true_type{});
       else tile(tb, std::false_type{});
     }
@@ -701,6 +726,16 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
         v += sc * mb[(w * 8 + h) * PS + (c == D ? D + 1 : c)];
       }
     }
+    if constexpr (WIN) {
+      if (out != nullptr) {  // the merged row goes on to finish_rows
+        float* fin = mb + NW * 8 * PS + h * finish_stride<D>();
+        if (in_bounds(NW * 8 * PS + (h + 1) * finish_stride<D>() <= SM::kRing / 4, status)) {
+          fin[c] = v;
+          if (c == D) fin[D + 1] = M;
+        }
+        continue;
+      }
+    }
     if (out != nullptr) {  // single chunk: the merged row goes on to the rotation below
       if (in_bounds(NW * 8 * PS + h * (D + 1) + c < SM::kRing / 4, status))
         mb[NW * 8 * PS + h * (D + 1) + c] = v;
@@ -715,6 +750,11 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
     }
   }
   if (out == nullptr) return;
+  if constexpr (WIN) {
+    finish_rows<D, NW>(mb + NW * 8 * PS, nh, n_splits, row_off, params + (size_t)hk * D * 4, out,
+                       (size_t)s * n_q * n_q_heads, q_rows, win.out_dtype, status);
+    return;
+  }
   // ---- a9 for a single chunk: o = acc / l, inverse SO(4) blocks, inverse WHT, as the
   // combine computes it for one part (bitwise the same); a warp per row
   __syncthreads();
@@ -738,10 +778,7 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
     const size_t ob = ((size_t)s * n_q_heads + row_off[h]) * D + lane * E;
     if (!in_bounds(ob + E <= out_len, status)) continue;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      if constexpr (WIN) store_typed(out, ob + i, y[i] * rs, win.out_dtype);
-      else static_cast<float*>(out)[ob + i] = y[i] * rs;
-    }
+    for (int i = 0; i < E; ++i) static_cast<float*>(out)[ob + i] = y[i] * rs;
   }
 }
 
@@ -761,12 +798,12 @@ cudaError_t launch_i8_t(const DecodeArgs& a, cudaStream_t stream, void* direct_o
   }
   const int G = a.n_q_heads / a.n_kv_heads;
   dim3 grid(a.n_splits, a.n_kv_heads * ((a.n_q * G + RB - 1) / RB), a.n_seqs);
-  decode_i8_kernel<D, NST, RB, TQ, MQ, NW, WIN><<<grid, NW * 32, SM::kBytes, stream>>>(
-      a.params, a.blocks, a.page_table, a.n_pages, a.max_pages, a.n_kv_heads,
+  return launch_clustered(
+      decode_i8_kernel<D, NST, RB, TQ, MQ, NW, WIN>, grid, NW * 32, SM::kBytes, stream,
+      WIN && direct_out != nullptr ? a.n_splits : 1, a.params, a.blocks, a.page_table, a.n_pages, a.max_pages, a.n_kv_heads,
       static_cast<const TQ*>(a.Q), a.n_q_heads, a.n_q, a.seq_lens, a.scale, a.pages_per_split,
       a.n_splits, a.partials, a.status, direct_out,
       I8Mul{0xFFFFFFFFu}, win_args(a));
-  return cudaGetLastError();
 }
 
 // Wide CTAs (more warps, one CTA per SM) when the whole grid fits in one CTA per SM: the
@@ -774,12 +811,15 @@ cudaError_t launch_i8_t(const DecodeArgs& a, cudaStream_t stream, void* direct_o
 // one after another.
 template <int D, int NST, int RB, typename TQ, bool MQ, bool WIN>
 cudaError_t launch_i8_w(const DecodeArgs& a, cudaStream_t stream, void* direct_out) {
-  constexpr int kWide = D == 128 ? 16 : 8;
-  const int G = a.n_q_heads / a.n_kv_heads;
-  const long long ctas =
-      (long long)a.n_splits * a.n_kv_heads * ((a.n_q * G + RB - 1) / RB) * a.n_seqs;
-  if (ctas <= (long long)decode_i8_sms())
-    return launch_i8_t<D, NST, RB, TQ, MQ, kWide, WIN>(a, stream, direct_out);
+  constexpr int kWide = wide_warps(D);
+  bool wide = a.wide;
+  if constexpr (!WIN) {
+    const int G = a.n_q_heads / a.n_kv_heads;
+    const long long ctas =
+        (long long)a.n_splits * a.n_kv_heads * ((a.n_q * G + RB - 1) / RB) * a.n_seqs;
+    wide = ctas <= (long long)decode_i8_sms();
+  }
+  if (wide) return launch_i8_t<D, NST, RB, TQ, MQ, kWide, WIN>(a, stream, direct_out);
   return launch_i8_t<D, NST, RB, TQ, MQ, 4, WIN>(a, stream, direct_out);
 }
 
@@ -787,7 +827,7 @@ template <int D, int NST, int RB, typename TQ>
 cudaError_t launch_i8_q(const DecodeArgs& a, cudaStream_t stream, void* direct_out) {
   const bool mq = a.n_q > 1;
   if (a.window > 0)
-    return mq ? launch_i8_w<D, NST, RB, TQ, true, true>(a, stream, nullptr)
+    return mq ? launch_i8_w<D, NST, RB, TQ, true, true>(a, stream, direct_out)
               : launch_i8_w<D, NST, RB, TQ, false, true>(a, stream, direct_out);
   return mq ? launch_i8_w<D, NST, RB, TQ, true, false>(a, stream, nullptr)
             : launch_i8_w<D, NST, RB, TQ, false, false>(a, stream, direct_out);
@@ -819,8 +859,9 @@ cudaError_t launch_i8_rb(const DecodeArgs& a, cudaStream_t stream, void* direct_
 cudaError_t launch_decode_split_i8(const DecodeArgs& a, cudaStream_t stream, bool* combined) {
   if (combined) *combined = false;
   if (a.bits != 3) return cudaErrorInvalidValue;
-  const bool direct = ISOQ_I8_DIRECT && combined && a.n_splits == 1 && a.n_q == 1 &&
-                      a.state == nullptr && a.out != nullptr;
+  const bool direct = a.window > 0 ? a.in_cluster
+                                   : ISOQ_I8_DIRECT && combined && a.n_splits == 1 && a.n_q == 1 &&
+                                         a.state == nullptr && a.out != nullptr;
   void* out = direct ? a.out : nullptr;
   const int rb = decode_rows_per_block(a.d, a.n_q, a.n_q_heads / a.n_kv_heads);
   cudaError_t e = cudaErrorInvalidValue;

@@ -32,6 +32,7 @@
 
 #include "isoq_check.cuh"
 #include "isoq_common.cuh"
+#include "isoq_finish.cuh"
 #include "isoq_internal.h"
 #include "isoq_ptx.cuh"
 #include "isoq_window.cuh"
@@ -43,15 +44,16 @@ using namespace ptx;
 // Dynamic shared memory: [kWarps][NST] page stages of block_bytes(D), then the mbarriers,
 // then the score mma's A fragments of the rotated queries (one uint4 per k-step and lane,
 // shared by the four warps).  The stage area is reused for the final merge.
-template <int D, int NST, int BITS = 3>
+template <int D, int NST, int BITS = 3, int NW = kWarps>
 struct MmaSmem {
   static constexpr int kStageBytes = block_bytes(D, BITS);
-  static constexpr int kRing = kWarps * NST * kStageBytes;
+  static constexpr int kRing = NW * NST * kStageBytes;
   static constexpr int kBarOff = kRing;
-  static constexpr int kAOff = kBarOff + kWarps * NST * 8;
+  static constexpr int kAOff = kBarOff + NW * NST * 8;
   static constexpr int kRowOff = kAOff + (D / 16) * 32 * 16;  // int [8]: output row per CTA row
   static constexpr int kBytes = kRowOff + 8 * 4;
-  static constexpr int kMergeBytes = kWarps * 8 * (D + 4) * 4;
+  // the warps' states [NW][8][D + 4] and the merged rows [8][D + 4]
+  static constexpr int kMergeBytes = NW * 8 * (D + 4) * 4 + 8 * (D + 4) * 4;
   static_assert(kMergeBytes <= kRing, "merge buffer must fit in the ring");
   static_assert(kAOff % 16 == 0, "A fragments must be 16-byte aligned");
 };
@@ -59,20 +61,22 @@ struct MmaSmem {
 // d = 128: <= 128 registers, 4 CTAs (16 warps) per SM; d = 256: two CTAs fill the shared
 // memory, so registers are not the limit
 template <int D>
-constexpr int dec_min_blocks() { return D == 128 ? 4 : 2; }
+constexpr int dec_min_blocks(int nw) { return nw != kWarps ? 1 : D == 128 ? 4 : 2; }
 
 // MQ: chunks of several query tokens per sequence with causal limits; the decode (one
 // query token, every row attending the whole context) is compiled without them.
-// WIN: sliding-window attention with sinks (isoq_window.cuh).
-template <int D, int NST, typename TQ, bool MQ, int BITS, bool WIN>
-__global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
+// WIN: sliding-window attention with sinks (isoq_window.cuh); with out, the chunks are the CTAs
+// of a cluster (or one CTA) and write the output rows (isoq_finish.cuh), and the wide CTAs
+// (NW > 4) hand a warp half a page at a time.
+template <int D, int NST, typename TQ, bool MQ, int BITS, bool WIN, int NW>
+__global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
     decode_mma_kernel(const float* __restrict__ params, const uint8_t* __restrict__ blocks,
                       const int32_t* __restrict__ page_table, int n_pages, int max_pages, int H,
                       const TQ* __restrict__ Q, int n_q_heads, int n_q,
                       const int32_t* __restrict__ seq_lens, float scale, int pages_per_split,
                       int n_splits, float* __restrict__ partials, uint32_t* status,
-                      const WinArgs win) {
-  using SM = MmaSmem<D, NST, BITS>;
+                      void* __restrict__ out, const WinArgs win) {
+  using SM = MmaSmem<D, NST, BITS, NW>;
   constexpr int E = D / 32;           // elements per lane in the warp WHT layout
   constexpr int NB = E / 4;
   constexpr int CB = code_bytes(D, BITS);
@@ -82,6 +86,7 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
   constexpr int KS = D / 16;          // k-steps of the score mma = m-tiles of the PV mma
   constexpr int NG = D / 128;         // 32-dim groups per thread and token (score: t, t+4)
   constexpr int PS = D + 4;
+  constexpr int SUB = WIN && NW != kWarps ? 2 : 1;  // tasks of a page
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
   uint4* qa = reinterpret_cast<uint4*>(smem + SM::kAOff);
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
   [[maybe_unused]] const size_t out_off0 = out_base - partials;
   if (tid < 8) row_off[tid] = tid < nh ? row_index(tid) : 0;
   __syncthreads();
-  if (p_begin >= p_end) {  // empty chunk: m = -inf, l = 0, acc = 0
+  if (p_begin >= p_end && !(WIN && out != nullptr)) {  // empty chunk: m = -inf, l = 0, acc = 0
     for (int i = tid; i < nh * PS; i += blockDim.x) {
       const int h = i / PS, c = i - h * PS;
       const size_t o = (size_t)row_off[h] * n_splits * PS + c;
@@ -143,15 +148,28 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
   }
   __syncwarp();
   const int* pt_row = page_table + (size_t)s * max_pages;
-  // page k of this warp: slot p_begin + warp + kWarps * k
-  const int n_my = (p_end - p_begin - warp + kWarps - 1) / kWarps;  // may be <= 0
+  // task k of this warp: page slot p_begin + (warp + NW * k) / SUB, its SUB-th part
+  const int n_my = (SUB * (p_end - p_begin) - warp + NW - 1) / NW;  // may be <= 0
   auto issue = [&](int k) {  // lane 0 only
-    const int pg = wp.page(p_begin + warp + kWarps * k);
+    const int pg = wp.page(p_begin + (warp + NW * k) / SUB);
     const int st = k % NST;
     const int phys = in_bounds(pg < max_pages && st < NST, status) ? __ldg(pt_row + pg) : -1;
     if (phys >= 0 && phys < n_pages && in_bounds(hk < H, status)) {
-      mbar_expect_tx(mybar + st, BB);
-      bulk_copy(myring + st * BB, blocks + ((size_t)phys * H + hk) * BB, BB, mybar + st);
+      const uint8_t* src = blocks + ((size_t)phys * H + hk) * BB;
+      uint8_t* dst = myring + st * BB;
+      mbar_expect_tx(mybar + st, BB / SUB);
+      if constexpr (SUB == 1) {
+        bulk_copy(dst, src, BB, mybar + st);
+      } else {  // 32 tokens' K codes, K norms, V codes and V norms, at their places in the block
+        const int part = (warp + NW * k) % SUB;
+        auto piece = [&](int off, int bytes) {
+          bulk_copy(dst + off + part * bytes, src + off + part * bytes, bytes, mybar + st);
+        };
+        piece(0, kPage * CB / SUB);
+        piece(k_norm_off(D, BITS), 2 * kPage / SUB);
+        piece(v_codes_off(D, BITS), kPage * CB / SUB);
+        piece(v_norm_off(D, BITS), 2 * kPage / SUB);
+      }
     } else {
       set_status(status, ISOQ_ST_PAGE_RANGE);
       mbar_arrive(mybar + st);  // complete the phase without data; tokens are masked
@@ -175,7 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
 #pragma unroll
     for (int k = 0; k < NB; ++k)
       if (in_bounds(hk < H && lane * NB + k < D / 4, status)) load_block_mat(hp, lane * NB + k, pq[k]);
-    for (int h = warp; h < 8; h += kWarps) {
+    for (int h = warp; h < 8; h += NW) {
       float v[E];
       if (h < nh && in_bounds((size_t)s * n_q * n_q_heads + row_off[h] < q_rows, status)) {
         const TQ* qp = Q + ((size_t)s * n_q * n_q_heads + row_off[h]) * D + lane * E;
@@ -233,7 +251,7 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
       break;
     }
     const uint8_t* blk = myring + st * BB;
-    const int pg = wp.page(p_begin + warp + kWarps * k);
+    const int pg = wp.page(p_begin + (warp + NW * k) / SUB);
     const int phys = in_bounds(pg < max_pages && st < NST, status) ? __ldg(pt_row + pg) : -1;
     const bool page_ok = phys >= 0 && phys < n_pages;
     const int tok0 = pg * kPage;
@@ -399,8 +417,14 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
         }
       }
     };
+    if constexpr (SUB == 1) {
 #pragma unroll
-    for (int tb = 0; tb < kPage; tb += 32) {
+      for (int tb = 0; tb < kPage; tb += 32) {
+        if (full) tile(tb, std::true_type{});
+        else tile(tb, std::false_type{});
+      }
+    } else {
+      const int tb = (warp + NW * k) % SUB * 32;
       if (full) tile(tb, std::true_type{});
       else tile(tb, std::false_type{});
     }
@@ -428,7 +452,7 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) lsum += __shfl_xor_sync(kFull, lsum, o);
   __syncthreads();  // all warps done with their rings
-  float* mb = reinterpret_cast<float*>(smem);  // [kWarps][8 heads][D + 4]
+  float* mb = reinterpret_cast<float*>(smem);  // [NW][8 heads][D + 4]
   {
     // acc_true = acc * sigma / ALPHA (times 1 / exp2(m2) in the log2 frame)
     const float f = sigma / ALPHA;
@@ -459,15 +483,25 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
     const int h = i / (D + 1), c = i - h * (D + 1);
     float M = -CUDART_INF_F;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mb[(w * 8 + h) * PS + D]);
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, mb[(w * 8 + h) * PS + D]);
     float v = 0.f;
     if (M != -CUDART_INF_F) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < NW; ++w) {
         const float mw = mb[(w * 8 + h) * PS + D];
         if (mw == -CUDART_INF_F) continue;
         const float sc = ex2(mw - M);
         v += sc * mb[(w * 8 + h) * PS + (c == D ? D + 1 : c)];
+      }
+    }
+    if constexpr (WIN) {
+      if (out != nullptr) {  // the merged row goes on to finish_rows
+        float* fin = mb + NW * 8 * PS + h * finish_stride<D>();
+        if (in_bounds(NW * 8 * PS + (h + 1) * finish_stride<D>() <= SM::kRing / 4, status)) {
+          fin[c] = v;
+          if (c == D) fin[D + 1] = M;
+        }
+        continue;
       }
     }
     float* o = out_base + (size_t)row_off[h] * n_splits * PS;
@@ -478,39 +512,50 @@ __global__ void __launch_bounds__(kWarps * 32, dec_min_blocks<D>())
       o[D + 1] = v;
     }
   }
+  if constexpr (WIN) {
+    if (out != nullptr)
+      finish_rows<D, NW>(mb + NW * 8 * PS, nh, n_splits, row_off, params + (size_t)hk * D * 4, out,
+                         (size_t)s * n_q * n_q_heads, q_rows, win.out_dtype, status);
+  }
 }
 
-template <int D, int NST, typename TQ, bool MQ, int BITS, bool WIN>
+template <int D, int NST, typename TQ, bool MQ, int BITS, bool WIN, int NW>
 static cudaError_t launch_mma_t(const DecodeArgs& a, cudaStream_t stream) {
-  using SM = MmaSmem<D, NST, BITS>;
+  using SM = MmaSmem<D, NST, BITS, NW>;
   // the dynamic shared-memory opt-in is per function and per device
   static unsigned long long attr_set = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !((attr_set >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(decode_mma_kernel<D, NST, TQ, MQ, BITS, WIN>,
+    e = cudaFuncSetAttribute(decode_mma_kernel<D, NST, TQ, MQ, BITS, WIN, NW>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
   const int G = a.n_q_heads / a.n_kv_heads;
   dim3 grid(a.n_splits, a.n_kv_heads * ((a.n_q * G + 7) / 8), a.n_seqs);
-  decode_mma_kernel<D, NST, TQ, MQ, BITS, WIN><<<grid, kWarps * 32, SM::kBytes, stream>>>(
-      a.params, a.blocks, a.page_table, a.n_pages, a.max_pages, a.n_kv_heads,
+  void* out = WIN && a.in_cluster ? a.out : nullptr;
+  return launch_clustered(
+      decode_mma_kernel<D, NST, TQ, MQ, BITS, WIN, NW>, grid, NW * 32, SM::kBytes, stream,
+      out != nullptr ? a.n_splits : 1, a.params, a.blocks, a.page_table, a.n_pages, a.max_pages, a.n_kv_heads,
       static_cast<const TQ*>(a.Q), a.n_q_heads, a.n_q, a.seq_lens, a.scale, a.pages_per_split,
-      a.n_splits, a.partials, a.status, win_args(a));
-  return cudaGetLastError();
+      a.n_splits, a.partials, a.status, out, win_args(a));
 }
 
 template <int D, int NST, int BITS, typename TQ>
 static cudaError_t launch_mma_q(const DecodeArgs& a, cudaStream_t stream) {
   const bool mq = a.n_q > 1;
+  constexpr int kWide = wide_warps(D);
+  constexpr int kWideStages = BITS == 2 ? 2 : 1;  // what the shared memory holds
+  if (a.window > 0 && a.wide)
+    return mq ? launch_mma_t<D, kWideStages, TQ, true, BITS, true, kWide>(a, stream)
+              : launch_mma_t<D, kWideStages, TQ, false, BITS, true, kWide>(a, stream);
   if (a.window > 0)
-    return mq ? launch_mma_t<D, NST, TQ, true, BITS, true>(a, stream)
-              : launch_mma_t<D, NST, TQ, false, BITS, true>(a, stream);
-  return mq ? launch_mma_t<D, NST, TQ, true, BITS, false>(a, stream)
-            : launch_mma_t<D, NST, TQ, false, BITS, false>(a, stream);
+    return mq ? launch_mma_t<D, NST, TQ, true, BITS, true, kWarps>(a, stream)
+              : launch_mma_t<D, NST, TQ, false, BITS, true, kWarps>(a, stream);
+  return mq ? launch_mma_t<D, NST, TQ, true, BITS, false, kWarps>(a, stream)
+            : launch_mma_t<D, NST, TQ, false, BITS, false, kWarps>(a, stream);
 }
 
 template <int D, int NST, int BITS>
@@ -564,11 +609,11 @@ int decode_resident_ctas(int d) {
       e = cudaSuccess;
     } else {
       using SM = MmaSmem<128, ISOQ_DEC_NST128, 4>;
-      e = cudaFuncSetAttribute(decode_mma_kernel<128, ISOQ_DEC_NST128, __nv_bfloat16, false, 4, false>,
+      e = cudaFuncSetAttribute(decode_mma_kernel<128, ISOQ_DEC_NST128, __nv_bfloat16, false, 4, false, kWarps>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kBytes);
       if (e == cudaSuccess)
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-            &n, decode_mma_kernel<128, ISOQ_DEC_NST128, __nv_bfloat16, false, 4, false>, kWarps * 32, SM::kBytes);
+            &n, decode_mma_kernel<128, ISOQ_DEC_NST128, __nv_bfloat16, false, 4, false, kWarps>, kWarps * 32, SM::kBytes);
     }
     if (e != cudaSuccess || n < 1) {
       cudaGetLastError();

@@ -80,6 +80,8 @@ struct DecodeArgs {
   int window;           // > 0: sliding-window attention over the last `window` tokens ...
   int n_sinks;          // ... and the first n_sinks; 0: the whole context
   int max_len;          // the bound of the lengths that the split plan was made for
+  bool in_cluster;      // window, row-block kernels: the chunks are one cluster, no partials
+  bool wide;            // ... of wide_warps(d) warps a CTA instead of 4
   float* state;         // if set: merged state [n_seqs][n_q][n_q_heads][d + 4] instead of out
   uint32_t* status;
 };
@@ -143,6 +145,28 @@ inline int attention_rows_per_cta(int d, int n_q, int group) {
   const long long rows = (long long)n_q * group;
   if (d != 128 || n_q <= 1 || rows < 16) return 8;
   return rows >= ISOQ_MQTC_MIN_ROWS ? 128 : 64;
+}
+
+// Warps of the row-block kernels' wide CTAs (grids with no more CTAs than SMs).
+constexpr int wide_warps(int d) { return d == 128 ? 16 : 8; }
+
+// A kernel launch with clusters of `cluster` CTAs along x (1: none).
+template <typename... P, typename... A>
+cudaError_t launch_clustered(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, int cluster, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 // Windowed chunks with more than 32 rows per KV head (d = 128) take the tensor-memory kernel,

@@ -123,6 +123,14 @@ DECODE = [
     dict(lens=[500, 1, 900], hq=12, hkv=3, W=250, S=70, bits=2, rot=1),
     dict(lens=[5000, 4700, 4999], hq=64, hkv=8, W=4096, S=4),
     dict(lens=[9000], hq=8, hkv=1, W=8192, S=0, out="f16"),
+    # more (sequence, KV head) units than SMs, chunks as clusters of 4-warp CTAs or one CTA each
+    dict(lens=list(range(0, 1200, 30)), hq=32, hkv=8, W=700, S=4),
+    dict(lens=list(range(5, 645, 16)), hq=15, hkv=5, W=300, S=70, bits=4, out="f16"),
+    dict(lens=list(range(0, 1400, 70)), hq=16, hkv=8, W=900, S=1, d=256),
+    # few units and a long window: partial results and the combine
+    dict(lens=[40000], hq=4, hkv=1, W=38000, S=4),
+    dict(lens=[33000, 10], hq=2, hkv=1, W=32000, S=0, bits=2, out="f16"),
+    dict(lens=[30000], hq=2, hkv=1, W=29999, S=1, d=256, out="f32"),
 ]
 
 
