@@ -328,14 +328,14 @@ def _check_read(cache, seq_ids, positions, K, V):
     first = V if K is None else K
     if first is None:
         raise ValueError("K or V must be given")
-    n, dev = seq_ids.numel(), cache.blocks.device
+    n, dev = seq_ids.numel(), cache.blocks.get_device()
     if seq_ids.dim() != 1 or positions.shape != seq_ids.shape:
         raise ValueError("seq_ids and positions must be of one length")
     for x in (K, V):
         if x is not None and (x.shape != (n, cache.n_kv_heads, cache.d) or x.dtype != first.dtype):
             raise ValueError(f"K and V must be [{n}][{cache.n_kv_heads}][{cache.d}] of one dtype")
-    if any(x is not None and x.device != dev for x in (seq_ids, positions, K, V)):
-        raise ValueError(f"seq_ids, positions, K and V must be on the cache's device {dev}")
+    if dev < 0 or any(x is not None and x.get_device() != dev for x in (seq_ids, positions, K, V)):
+        raise ValueError("seq_ids, positions, K and V must be on the cache's device")
     return first
 
 
@@ -358,7 +358,7 @@ def isoq_dequantize_rope(params: Params, cache: PagedCache, seq_ids, positions, 
     import torch
     first = _check_read(cache, seq_ids, positions, K, V)
     if rope_table.dim() != 3 or rope_table.shape[1:] != (cache.d // 2, 2) or \
-            rope_table.device != cache.blocks.device:
+            rope_table.get_device() != cache.blocks.get_device():
         raise ValueError(f"rope_table must be [max_pos][{cache.d // 2}][2] on the cache's device")
     _check(_lib.isoq_dequantize_rope(
         params.handle, cache._c, _dev_ptr(seq_ids, "seq_ids", torch.int32),
@@ -435,9 +435,10 @@ def _check_window(cache, Q, seq_lens, out, workspace):
         raise ValueError(f"Q and out must have the same shape ending in d = {cache.d}")
     if seq_lens.numel() < Q.shape[0]:
         raise ValueError("seq_lens must have one entry per sequence")
-    dev = cache.blocks.device
-    if not (Q.device == out.device == seq_lens.device == workspace.device == dev):
-        raise ValueError(f"Q, seq_lens, out and workspace must be on the cache's device {dev}")
+    dev = cache.blocks.get_device()
+    if dev < 0 or not (Q.get_device() == out.get_device() == seq_lens.get_device() ==
+                       workspace.get_device() == dev):
+        raise ValueError("Q, seq_lens, out and workspace must be on the cache's device")
 
 
 def isoq_decode_attention_window(params: Params, cache: PagedCache, Q, seq_lens, max_seq_len: int,

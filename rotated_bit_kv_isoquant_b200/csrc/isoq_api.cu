@@ -72,28 +72,26 @@ void hamilton(const double* a, const double* b, double* o) {
 // kRotScale R[k][n] split into two binary16 parts, hi + lo, each in the tensor core's
 // no-swizzle K-major layout.  [head][half q][part][k / 8][n / 8][n % 8][k % 8].  R in
 // binary64 from the 4x4 block matrices: R[k][n] = sum_j M[k][j] H[4 (k/4) + j][n] / sqrt(d).
-std::vector<__half> rotation_parts(const std::vector<float>& mats, int d, int n_kv_heads) {
-  const size_t part = (size_t)d * 128;
-  std::vector<__half> out((size_t)n_kv_heads * d * d * 2);
+// One thread per entry.
+__global__ void rotation_parts_kernel(const float* __restrict__ mats, __half* __restrict__ out,
+                                      int d, int n_kv_heads) {
+  const size_t part = (size_t)d * 128, entries = (size_t)n_kv_heads * d * d;
   const double unit = isoq::kRotScale / sqrt((double)d);
-  for (int h = 0; h < n_kv_heads; ++h)
-    for (int q = 0; q < d / 128; ++q) {
-      __half* hi = out.data() + ((size_t)h * (d / 128) + q) * 2 * part;
-      for (int k = 0; k < d; ++k) {
-        const float* M = mats.data() + ((size_t)h * (d / 4) + k / 4) * 16 + (k & 3) * 4;
-        for (int n = 0; n < 128; ++n) {
-          const int dim = isoq::read_column(d, q, n);
-          double r = 0.0;
-          for (int j = 0; j < 4; ++j)  // Sylvester: H[a][b] = (-1)^popcount(a & b)
-            r += (__builtin_popcount((4 * (k / 4) + j) & dim) & 1) ? -(double)M[j] : (double)M[j];
-          r *= unit;
-          const size_t at = (size_t)(k / 8) * 1024 + (n / 8) * 64 + (n % 8) * 8 + k % 8;
-          hi[at] = __float2half_rn((float)r);
-          hi[part + at] = __float2half_rn((float)(r - (double)__half2float(hi[at])));
-        }
-      }
-    }
-  return out;
+  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < entries;
+       i += (size_t)gridDim.x * blockDim.x) {
+    const size_t hq = i / part;  // head * (d / 128) + q
+    const int k = (int)(i % part) / 128, n = (int)(i % 128);
+    const int h = (int)(hq / (d / 128)), q = (int)(hq % (d / 128));
+    const int dim = isoq::read_column(d, q, n);
+    const float* M = mats + ((size_t)h * (d / 4) + k / 4) * 16 + (k & 3) * 4;
+    double r = 0.0;
+    for (int j = 0; j < 4; ++j)  // Sylvester: H[a][b] = (-1)^popcount(a & b)
+      r += (__popc((4 * (k / 4) + j) & dim) & 1) ? -(double)M[j] : (double)M[j];
+    r *= unit;
+    __half* hi = out + hq * 2 * part + (size_t)(k / 8) * 1024 + (n / 8) * 64 + (n % 8) * 8 + k % 8;
+    hi[0] = __float2half_rn((float)r);
+    hi[part] = __float2half_rn((float)(r - (double)__half2float(hi[0])));
+  }
 }
 
 // SM count of the current device (148 on B200 when no device can be queried, which keeps
@@ -195,12 +193,15 @@ int window_pages(int n_q_heads, int n_kv_heads, int d, int max_seq_len, int n_q,
 //   4-warp CTAs with partial results in the workspace and the combine, any number to a unit
 // The one with the smallest estimated time is taken.  The estimate, in us, fitted to sweeps of
 // all three over 1 to 64 sequences, windows of 512 to 131072 tokens and d = 128 and 256 (within
-// 15% of most): a start of 2.5, a CTA's rotation and merge of 6.5, a page's step of one warp of
+// 15% of most): a start of 2.5, a CTA's rotation and merge of 6.5 (of 12 for a chunk of query
+// tokens, whose CTAs also find their rows and limits), a page's step of one warp of
 // 1.75 alone to 4.75 with every warp of the SM busy, 0.3 for the cluster's exchange, 1.2 for the
 // combine, waves of CTAs one after another.  E.g. (wide, 4-warp cluster, partials; best of
 // each): 1 sequence x 4 KV heads x 17 pages 9.3, 9.4, 10.1; 8 x 8 x 66 20.1, 21.5, 22.3;
-// 64 x 8 x 129 192, 155, 157; 1 x 8 x 2048 91, 129, 48.
-SplitPlan plan_row_blocks(long long units, int d, int pages) {
+// 64 x 8 x 129 192, 155, 157; 1 x 8 x 2048 91, 129, 48; 16 x 8 x 3 row blocks of a 5-token chunk
+// x 66 88, 75, 86.
+SplitPlan plan_row_blocks(long long units, int d, int pages, bool chunk) {
+  const double cta_us = chunk ? 12.0 : 6.5;
   const int sms = sm_count(), per_sm = isoq::decode_i8_resident_ctas(d);
   const int narrow = sms * per_sm, warps = isoq::wide_warps(d);
   SplitPlan best{1, pages, true, false};
@@ -215,12 +216,12 @@ SplitPlan plan_row_blocks(long long units, int d, int pages) {
       // one CTA takes an SM, and a cluster lies within one of the GPCs of 16 to 18 SMs: sizes
       // that divide them, with room for what 4 and 8 leave over
       if ((parts & (parts - 1)) != 0 || ctas > (parts <= 2 ? sms : sms - sms / 8)) return;
-      us += 6.5 + 0.5 * ((2 * pps + warps - 1) / warps) * page_us(2.0 * pps / warps);
+      us += cta_us + 0.5 * ((2 * pps + warps - 1) / warps) * page_us(2.0 * pps / warps);
     } else {
       const int steps = (pps + 3) / 4;
       const double full = floor(ctas / narrow), rest = ctas - full * narrow;
-      us += full * (6.5 + steps * page_us(1));
-      if (rest > 0) us += 6.5 + steps * page_us(ceil(rest / sms) / per_sm);
+      us += full * (cta_us + steps * page_us(1));
+      if (rest > 0) us += cta_us + steps * page_us(ceil(rest / sms) / per_sm);
     }
     if (pps <= isoq::kMaxPagesPerSplit && (best_us < 0 || us < best_us)) {
       best_us = us;
@@ -246,7 +247,7 @@ SplitPlan plan_window(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_
   if (!isoq::use_window_tc(d, n_q, G)) {
     const int RB = isoq::decode_rows_per_block(d, n_q, G);
     return plan_row_blocks((long long)n_seqs * n_kv_heads * (((long long)n_q * G + RB - 1) / RB), d,
-                           pages);
+                           pages, n_q > 1);
   }
   // The tensor-memory kernel runs one CTA per SM: the number of chunks with the smallest time
   // in units of a page's (~2 us).  Rounds of CTAs, each the pages of a chunk plus a start and
@@ -388,18 +389,20 @@ int isoq_make_params_v(uint64_t seed, int d, int n_kv_heads, int bits, int rotat
       for (int i = 0; i < 4; ++i) M[i * 4 + j] = (float)z[i];
     }
   }
-  const std::vector<__half> rot = rotation_parts(mats, d, n_kv_heads);
   const size_t rot_off = ((nq + mats.size()) * sizeof(float) + 255) / 256 * 256;
-  e = cudaMalloc(&p->dev, rot_off + rot.size() * sizeof(__half));
+  e = cudaMalloc(&p->dev, rot_off + (size_t)n_kv_heads * d * d * 2 * sizeof(__half));
   if (e == cudaSuccess) {
     p->dev_mat = p->dev + nq;
     p->dev_rot = reinterpret_cast<__half*>(reinterpret_cast<char*>(p->dev) + rot_off);
     e = cudaMemcpy(p->dev, p->host.data(), nq * sizeof(float), cudaMemcpyHostToDevice);
   }
   if (e == cudaSuccess)
-    e = cudaMemcpy(p->dev_rot, rot.data(), rot.size() * sizeof(__half), cudaMemcpyHostToDevice);
-  if (e == cudaSuccess)
     e = cudaMemcpy(p->dev_mat, mats.data(), mats.size() * sizeof(float), cudaMemcpyHostToDevice);
+  if (e == cudaSuccess) {
+    rotation_parts_kernel<<<512, 256>>>(p->dev_mat, p->dev_rot, d, n_kv_heads);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+  }
   if (e != cudaSuccess) {
     if (p->dev) cudaFree(p->dev);
     delete p;

@@ -45,9 +45,9 @@ __device__ __forceinline__ constexpr uint32_t col_s(int w) { return 64 * w; }
 __device__ __forceinline__ constexpr uint32_t col_p(int w) { return 128 + 32 * w; }
 __device__ __forceinline__ constexpr uint32_t col_o(int w) { return 256 + 128 * w; }
 
-enum Bar {  // mbarriers, two of each (by ring / tile stage, or by softmax half)
-  kRing = 0, kKFull = 2, kVFull = 4, kKFree = 6, kVFree = 8,
-  kSFull = 10, kSRead = 12, kPFull = 14, kPvDone = 16, kDrain = 18, kBars = 19
+enum Bar {  // mbarriers: of the ring (2), the tile stages (up to 4), the softmax halves (2)
+  kRing = 0, kKFull = 2, kVFull = 6, kKFree = 10, kVFree = 14,
+  kSFull = 18, kSRead = 20, kPFull = 22, kPvDone = 24, kDrain = 26, kBars = 27
 };
 
 template <int BITS>
@@ -59,9 +59,9 @@ struct WinSmem {
   static constexpr int kOffK = 4 * kQPart;              // [2] K_hat tiles
   static constexpr int kOffV = kOffK + 2 * kPageTile;   // [2] V_hat tiles
   static constexpr int kOffRing = kOffV + 2 * kPageTile;
-  static constexpr int kOffNorm = kOffRing + 2 * kBB;   // float [2][64 K | 64 V]
-  static constexpr int kOffMeta = kOffNorm + 2 * 128 * 4;  // float [2] sigma, int [2] page is valid
-  static constexpr int kOffRed = kOffMeta + 16;         // float [2]
+  static constexpr int kOffNorm = kOffRing + 2 * kBB;   // float [4 stages][64 K | 64 V]
+  static constexpr int kOffMeta = kOffNorm + 4 * 128 * 4;  // float [4] sigma, int [4] page is valid
+  static constexpr int kOffRed = kOffMeta + 32;         // float [2]
   static constexpr int kOffMl = kOffRed + 16;           // float2 [2 halves][128]: m, l
   static constexpr int kOffRow = kOffMl + 256 * 8;      // int [256]: output row of each row
   static constexpr int kOffBar = kOffRow + 256 * 4;
@@ -69,6 +69,8 @@ struct WinSmem {
   static constexpr int kBytes = kOffTmem + 16;
   static_assert(kOffRing % 16 == 0 && kBB % 16 == 0 && kOffBar % 8 == 0 && kOffNorm % 16 == 0, "");
   static_assert(kBytes <= 227 * 1024, "shared memory");
+  // one row block leaves the second half's query tiles free: two more tile stages
+  static_assert(4 * kPageTile <= 2 * kQPart, "stages 2 and 3");
 };
 
 // wht_warp of a 128-dim vector with the lanes' signs at hand: one multiply-add per element and
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);
   float* nrm = reinterpret_cast<float*>(smem + SM::kOffNorm);
   float* sig = reinterpret_cast<float*>(smem + SM::kOffMeta);
-  int* valid = reinterpret_cast<int*>(smem + SM::kOffMeta) + 2;
+  int* valid = reinterpret_cast<int*>(smem + SM::kOffMeta) + 4;
   float* red = reinterpret_cast<float*>(smem + SM::kOffRed);
   float2* ml = reinterpret_cast<float2*>(smem + SM::kOffMl);
   int* row_off = reinterpret_cast<int*>(smem + SM::kOffRow);
@@ -234,6 +236,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
   tc::fence_after();
   const uint32_t tmem = __shfl_sync(kFull, *tmem_slot, 0);
   const int role = __shfl_sync(kFull, warp, 0);  // warp-uniform to the compiler as well
+  // tile stages: 2, or 4 with one row block; page k takes stage k % stages, phase k / stages
+  const int st_mask = two ? 1 : 3, st_log = two ? 1 : 2;
+  auto tile_k = [&](int st) { return st < 2 ? sK + st * kPageTile : sQ + 2 * SM::kQPart + (st - 2) * 2 * kPageTile; };
+  auto tile_v = [&](int st) { return st < 2 ? sV + st * kPageTile : tile_k(st) + kPageTile; };
   // jobs of softmax half w: page k = i with two row blocks, else k = 2 i + w
   auto jobs = [&](int w) { return two ? n : (n - w + 1) / 2; };
   bool ok = true;
@@ -252,15 +258,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
     int issued = min(n, 2), k = 0;
     bool page_nx = phys_of(0) >= 0;  // looked up a page ahead
     for (; k < n; ++k) {
-      const int st = k & 1;
-      const uint8_t* blk = smem + SM::kOffRing + st * BB;
-      ok = mbar_wait(bars + kRing + st, (k >> 1) & 1) &&
-           (k < 2 || mbar_wait(bars + kKFree + st, ((k - 2) >> 1) & 1));
-      if (ok) page_tile<BITS>(blk, 0, t, sK + st * kPageTile, tl0, tl1, th0, th1, status);
+      const int st = k & st_mask;
+      const int before = k - st_mask - 1;  // the page that had the stage
+      const int ph_before = (before >> st_log) & 1;
+      const uint8_t* blk = smem + SM::kOffRing + (k & 1) * BB;
+      ok = mbar_wait(bars + kRing + (k & 1), (k >> 1) & 1) &&
+           (before < 0 || mbar_wait(bars + kKFree + st, ph_before));
+      if (ok) page_tile<BITS>(blk, 0, t, tile_k(st), tl0, tl1, th0, th1, status);
       fence_proxy_async();  // the generic-proxy tile writes, before the tensor core reads
       if (ok) mbar_arrive(bars + kKFull + st);
-      // the V tile, the norms and sigma of page k - 2 have been used once its value product is done
-      ok = ok && (k < 2 || mbar_wait(bars + kVFree + st, ((k - 2) >> 1) & 1));
+      // the V tile, the norms and sigma of the page before have been used once its value product
+      // is done
+      ok = ok && (before < 0 || mbar_wait(bars + kVFree + st, ph_before));
       // nrm[j] = |k_j| kf; nrm[64 + j] = |v_j| / sigma with the CTA's V-norm reference sigma (it
       // only scales the weights), raised when a token some row sees has |v| > kSigmaSlack sigma
       const int tok0 = wp.page(p_begin + k) * kPage;
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
           }
         }
       }
-      if (ok) page_tile<BITS>(blk, 1, t, sV + st * kPageTile, tl0, tl1, th0, th1, status);
+      if (ok) page_tile<BITS>(blk, 1, t, tile_v(st), tl0, tl1, th0, th1, status);
       fence_proxy_async();
       if (ok) mbar_arrive(bars + kVFull + st);
       // the ring stage (and red) has been read; whether one of the 128 threads gave up
@@ -317,7 +326,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     // a7: S_h(k), 8 k-steps of 16 dims, the high and the low part
     auto scores = [&](int h, int k) {
       const uint64_t q = tc::sdesc(sQ + (two ? h : 0) * 2 * SM::kQPart, SM::kQGroup, 128);
-      const uint64_t kt = tc::sdesc(sK + (k & 1) * kPageTile, 1024, 128);
+      const uint64_t kt = tc::sdesc(tile_k(k & st_mask), 1024, 128);
       tc::fence_after();
       if (one) {
 #pragma unroll
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     };
     // a8: O_h += P'_h . V_hat(k), 4 k-steps of 16 tokens; i = the half's job number
     auto values = [&](int h, int k, int i) {
-      const uint64_t vt = tc::sdesc(sV + (k & 1) * kPageTile, 2048, 128);
+      const uint64_t vt = tc::sdesc(tile_v(k & st_mask), 2048, 128);
       tc::fence_after();
       if (one) {
 #pragma unroll
@@ -370,15 +379,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
         commit(kKFree + k);
       }
       for (int k = 0; ok && k < n; ++k) {
-        const int h = k & 1, i = k >> 1;  // also the tile stage and its phase
+        const int h = k & 1, i = k >> 1, st = k & 3, st2 = (k + 2) & 3;
         if (k + 2 < n) {
-          if (!(ok = wait(kKFull + h, i + 1) && wait(kSRead + h, i))) break;
+          if (!(ok = wait(kKFull + st2, (k + 2) >> 2) && wait(kSRead + h, i))) break;
           scores(h, k + 2);
-          commit(kKFree + h);
+          commit(kKFree + st2);
         }
-        if (!(ok = wait(kVFull + h, i) && wait(kPFull + h, i))) break;
+        if (!(ok = wait(kVFull + st, k >> 2) && wait(kPFull + h, i))) break;
         values(h, k, i);
-        commit(kVFree + h);
+        commit(kVFree + st);
       }
     }
     if (!ok) {  // gave up: wait (bounded) for the products in flight
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const uint32_t t_s = t_lane + col_s(w), t_p = t_lane + col_p(w), t_o = t_lane + col_o(w);
     const int n_jobs = jobs(w);
     for (int i = 0; i < n_jobs; ++i) {
-      const int k = two ? i : 2 * i + w, st = k & 1;
+      const int k = two ? i : 2 * i + w, st = k & st_mask;
       // the page's scores (warp-uniform: collective loads follow), then its norms
       ok = __all_sync(kFull, mbar_wait(bars + kSFull + w, i & 1));
       if (!ok) break;
@@ -407,7 +416,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       tc::fence_before();
       mbar_arrive(bars + kSRead + w);
-      ok = __all_sync(kFull, mbar_wait(bars + kVFull + st, (k >> 1) & 1));
+      ok = __all_sync(kFull, mbar_wait(bars + kVFull + st, (k >> st_log) & 1));
       if (!ok) break;
       const float* nk = nrm + st * 128;
       const bool page_ok = valid[st] != 0;
