@@ -1,5 +1,5 @@
-// One page of a (page, KV head) block at d = 128 dequantised by 128 threads into the tensor
-// cores' no-swizzle shared-memory operand of 64 tokens x 128 dims in binary16.
+// One page of a (page, KV head) block at d = 128 dequantised by NT threads into the tensor cores'
+// no-swizzle shared-memory operand of 64 tokens x 128 dims in binary16.
 #pragma once
 
 #include "isoq_check.cuh"
@@ -18,18 +18,19 @@ __device__ __forceinline__ void st_v4(uint32_t addr, const uint32_t (&o)[4]) {
                : "memory");
 }
 
-// blk: the block in shared memory; tid 0..127.  kv = 0: K_hat, K-major (B of the scores, N = 64
+// blk: the block in shared memory; tid 0 .. NT-1, whole warps.  kv = 0: K_hat, K-major (B of the scores, N = 64
 // tokens): (dim/8) 1024 + (tok/8) 128 + (tok%8) 16 + (dim%8) 2.  kv = 1: V_hat, MN-major (B of
 // the value product, K = 64 tokens): (tok/8) 2048 + (dim/8) 128 + (tok%8) 16 + (dim%8) 2.
 // Values are ALPHA times the levels; tl0 .. th1 are the format's level tables.
-template <int BITS>
+template <int BITS, int NT = 128>
 __device__ __forceinline__ void page_tile(const uint8_t* blk, int kv, int tid, uint32_t tile,
                                           uint32_t tl0, uint32_t tl1, uint32_t th0, uint32_t th1,
                                           uint32_t* status) {
   constexpr int D = 128, CB = code_bytes(D, BITS), W = BITS;
 #pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    const int u = tid + 128 * hf;
+  for (int hf = 0; hf < (256 + NT - 1) / NT; ++hf) {
+    const int u = tid + NT * hf;
+    if (256 % NT != 0 && u >= 256) break;
     if (BITS == 3 && kv == 1) {
       // V tile layout: u = (block, quad, 8-dim unit) group of four tokens.  Lanes 4m ..
       // 4m+3 take quads 0-3 of one unit, so a warp's 12-byte group loads hit 32 distinct

@@ -3,10 +3,11 @@
 //
 // As in the other attention kernels the queries are rotated once, scores and value sum run on
 // codebook levels in the rotated space, and a row is a (query token, query head) pair; what a
-// row sees is isoq_window.cuh's.  One CTA per SM of 13 warps works on one context chunk of one
+// row sees is isoq_window.cuh's.  One CTA per SM of 16 warps works on one context chunk of one
 // KV head:
-//   warps 8-11   take the page blocks from a 2-stage ring (1-D bulk copies) and dequantise
-//                K_hat and V_hat into two f16 operand tiles each, with the page's norms
+//   warps 8-11   take the page blocks from a 2-stage ring (1-D bulk copies), dequantise K_hat into
+//                f16 operand tiles and give the page's norms
+//   warps 13-15  dequantise V_hat
 //   warp 12      one thread issues the products: scores S = Q~hi K_hat^T + Q~lo K_hat^T and
 //                O += P' V_hat, accumulators in tensor memory
 //   warps 0-3,   softmax: thread r owns row r of its half (tensor-memory lane r), reads its 64
@@ -38,7 +39,8 @@ using namespace ptx;
 namespace {
 
 constexpr int kWD = 128;
-constexpr int kWThreads = 13 * 32;
+constexpr int kWWarps = 16, kWThreads = kWWarps * 32;
+constexpr int kWK = 128, kWV = 96;  // threads that dequantise K_hat (and the norms), V_hat
 // tensor-memory columns: S 64, P' 32 and O 128 of each half
 constexpr uint32_t kWCols = 512;
 __device__ __forceinline__ constexpr uint32_t col_s(int w) { return 64 * w; }
@@ -171,8 +173,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
   };
   if (tid == 256) {
     for (int i = 0; i < kBars; ++i) {
-      const bool many = (i >= kKFull && i < kKFree) || (i >= kSRead && i < kPvDone);
-      mbar_init(bars + i, many ? 128 : 1);
+      // arrivals: the K threads; theirs (norms) and the V threads; a softmax half; else one
+      mbar_init(bars + i, i >= kKFull && i < kVFull   ? kWK
+                          : i >= kVFull && i < kKFree ? kWK + kWV
+                          : i >= kSRead && i < kPvDone ? 128 : 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     issue(0);
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   for (int i = 0; i < 5; ++i) sgn[i] = ((lane >> i) & 1) ? -1.f : 1.f;
   __syncthreads();  // the rows' places
   // ---- a6: rotate the rows' queries into the A tiles (f16 high and low parts) ------------
-  if (warp < 12) {
+  {
     float M[16];
     load_block_mat(params + (size_t)hk * D * 4, lane, M);
     const int k0 = lane * E;  // dims 4 lane .. + 3: half of one 16-byte core-matrix row
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     auto load = [&](int r0, float (&v)[kAt][E]) {
 #pragma unroll
       for (int j = 0; j < kAt; ++j) {
-        const int r = r0 + 12 * j;
+        const int r = r0 + kWWarps * j;
 #pragma unroll
         for (int i = 0; i < E; ++i) v[j][i] = 0.f;
         if (r < nh && in_bounds(row_off[r] < n_q * n_q_heads, status))
@@ -203,18 +207,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
     float nx[kAt][E];
     load(warp, nx);
 #pragma unroll 1
-    for (int r0 = warp; r0 < rows_cta; r0 += 12 * kAt) {
+    for (int r0 = warp; r0 < rows_cta; r0 += kWWarps * kAt) {
       float v[kAt][E];
 #pragma unroll
       for (int j = 0; j < kAt; ++j)
 #pragma unroll
         for (int i = 0; i < E; ++i) v[j][i] = nx[j][i];
-      load(r0 + 12 * kAt, nx);
+      load(r0 + kWWarps * kAt, nx);
 #pragma unroll
       for (int j = 0; j < kAt; ++j) wht_signed(v[j], sgn);
 #pragma unroll
       for (int j = 0; j < kAt; ++j) {
-        const int r = r0 + 12 * j;
+        const int r = r0 + kWWarps * j;
         float z[E], hi[E];
         mat_fwd(M, v[j], z);
 #pragma unroll
@@ -249,9 +253,19 @@ __global__ void __launch_bounds__(kWThreads, 1)
   float m2 = -CUDART_INF_F, lsum = 0.f, sigma = 0.f;
   const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
 
-  if (role >= 8 && role < 12) {
+  // the ring stage has been read by the K and V threads; whether one of them gave up
+  auto ring_read = [&]() {
+    uint32_t gave_up;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, %2, p;\n"
+        " selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(gave_up) : "r"((uint32_t)!ok), "n"(kWK + kWV) : "memory");
+    return gave_up != 0;
+  };
+  if (role >= 8 && role != 12) {
     // ================ dequantisation ======================================================
-    const int t = tid - 256;
+    const bool k_side = role < 12;
+    const int t = tid - (k_side ? 256 : 416);
     uint32_t tl0, tl1, th0, th1;
     level_tables<BITS>(tl0, tl1, th0, th1);
     const float kf = scale * kLog2e / (ALPHA * (float)D);  // log2 score per (dot * nK)
@@ -262,49 +276,48 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const int before = k - st_mask - 1;  // the page that had the stage
       const int ph_before = (before >> st_log) & 1;
       const uint8_t* blk = smem + SM::kOffRing + (k & 1) * BB;
-      ok = mbar_wait(bars + kRing + (k & 1), (k >> 1) & 1) &&
-           (before < 0 || mbar_wait(bars + kKFree + st, ph_before));
-      if (ok) page_tile<BITS>(blk, 0, t, tile_k(st), tl0, tl1, th0, th1, status);
-      fence_proxy_async();  // the generic-proxy tile writes, before the tensor core reads
-      if (ok) mbar_arrive(bars + kKFull + st);
+      ok = mbar_wait(bars + kRing + (k & 1), (k >> 1) & 1);
+      if (k_side) {
+        ok = ok && (before < 0 || mbar_wait(bars + kKFree + st, ph_before));
+        if (ok) page_tile<BITS, kWK>(blk, 0, t, tile_k(st), tl0, tl1, th0, th1, status);
+        fence_proxy_async();  // the generic-proxy tile writes, before the tensor core reads
+        if (ok) mbar_arrive(bars + kKFull + st);
+      }
       // the V tile, the norms and sigma of the page before have been used once its value product
       // is done
       ok = ok && (before < 0 || mbar_wait(bars + kVFree + st, ph_before));
-      // nrm[j] = |k_j| kf; nrm[64 + j] = |v_j| / sigma with the CTA's V-norm reference sigma (it
-      // only scales the weights), raised when a token some row sees has |v| > kSigmaSlack sigma
-      const int tok0 = wp.page(p_begin + k) * kPage;
-      const bool page_ok = page_nx;
-      if (k + 1 < n) page_nx = phys_of(k + 1) >= 0;
-      if (t < 64) {
-        if (ok) nrm[st * 128 + t] = half_at(blk + k_norm_off(D, BITS) + 2 * t) * kf;
+      if (!k_side) {
+        if (ok) page_tile<BITS, kWV>(blk, 1, t, tile_v(st), tl0, tl1, th0, th1, status);
+        fence_proxy_async();
       } else {
-        const int j = t - 64;
-        float nv = half_at(blk + v_norm_off(D, BITS) + 2 * j);
-        nv = page_ok && tok0 + j < lim_hi && wp.any_sees(win, tok0 + j) ? nv : 0.f;
-        float pm = warp_max(nv);
-        if (lane == 0) red[warp - 10] = pm;
-        asm volatile("bar.sync 1, 64;" ::: "memory");  // warps 10 and 11
-        pm = fmaxf(red[0], red[1]);
-        sigma = pm > sigma * kSigmaSlack ? pm : sigma;
-        if (ok) {
-          nrm[st * 128 + t] = sigma > 0.f ? nv * (1.f / sigma) : 0.f;
-          if (t == 64) {
-            sig[st] = sigma;
-            valid[st] = page_ok;
+        // nrm[j] = |k_j| kf; nrm[64 + j] = |v_j| / sigma with the CTA's V-norm reference sigma (it
+        // only scales the weights), raised when a token some row sees has |v| > kSigmaSlack sigma
+        const int tok0 = wp.page(p_begin + k) * kPage;
+        const bool page_ok = page_nx;
+        if (k + 1 < n) page_nx = phys_of(k + 1) >= 0;
+        if (t < 64) {
+          if (ok) nrm[st * 128 + t] = half_at(blk + k_norm_off(D, BITS) + 2 * t) * kf;
+        } else {
+          const int j = t - 64;
+          float nv = half_at(blk + v_norm_off(D, BITS) + 2 * j);
+          nv = page_ok && tok0 + j < lim_hi && wp.any_sees(win, tok0 + j) ? nv : 0.f;
+          float pm = warp_max(nv);
+          if (lane == 0) red[warp - 10] = pm;
+          asm volatile("bar.sync 1, 64;" ::: "memory");  // warps 10 and 11
+          pm = fmaxf(red[0], red[1]);
+          sigma = pm > sigma * kSigmaSlack ? pm : sigma;
+          if (ok) {
+            nrm[st * 128 + t] = sigma > 0.f ? nv * (1.f / sigma) : 0.f;
+            if (t == 64) {
+              sig[st] = sigma;
+              valid[st] = page_ok;
+            }
           }
         }
       }
-      if (ok) page_tile<BITS>(blk, 1, t, tile_v(st), tl0, tl1, th0, th1, status);
-      fence_proxy_async();
       if (ok) mbar_arrive(bars + kVFull + st);
-      // the ring stage (and red) has been read; whether one of the 128 threads gave up
-      uint32_t gave_up;
-      asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, 128, p;\n"
-          " selp.u32 %0, 1, 0, q;\n}"
-          : "=r"(gave_up) : "r"((uint32_t)!ok) : "memory");
-      if (gave_up) break;
-      if (t == 0 && k + 2 < n) {
+      if (ring_read()) break;
+      if (tid == 256 && k + 2 < n) {
         fence_proxy_async();
         issue(k + 2);
       }
@@ -312,7 +325,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     }
     if (k < n) {  // gave up: wait (bounded) for the copies in flight
       ok = false;
-      if (t == 0)
+      if (tid == 256)
         for (int kk = k; kk < issued; ++kk) mbar_wait(bars + kRing + (kk & 1), (kk >> 1) & 1);
     }
   } else if (role == 12) {
@@ -527,16 +540,16 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
     }
     __syncthreads();
-    if (role < 12) {
+    {
       float M[16];
       load_block_mat(params + (size_t)hk * D * 4, lane, M);
       constexpr int kAt = 4;  // rows at a time
 #pragma unroll 1
-      for (int r0 = role; r0 < nh; r0 += 12 * kAt) {
+      for (int r0 = role; r0 < nh; r0 += kWWarps * kAt) {
         float y[kAt][E], m[kAt], l[kAt];
 #pragma unroll
         for (int j = 0; j < kAt; ++j) {
-          const int r = min(r0 + 12 * j, nh - 1);
+          const int r = min(r0 + kWWarps * j, nh - 1);
           const float2 a = ml[r];
           const float4 v = *at(r, lane);
           m[j] = a.x;
@@ -566,7 +579,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
 #pragma unroll
         for (int j = 0; j < kAt; ++j) {
-          const int r = r0 + 12 * j;
+          const int r = r0 + kWWarps * j;
           if (r >= nh) continue;
           const int ri = row_off[r];
           if (!in_bounds(ri < n_q * n_q_heads, status)) continue;
