@@ -152,6 +152,30 @@ __device__ __forceinline__ void wht_warp(float (&v)[E], int lane) {
   }
 }
 
+// The same with the lane's side of each cross-lane stage at hand (sgn[s] = -1 where bit s of
+// the lane is set, else 1): one exact multiply-add per element and stage, for kernels that
+// transform many vectors.
+template <int E>
+__device__ __forceinline__ void wht_signed(float (&v)[E], const float (&sgn)[5]) {
+#pragma unroll
+  for (int h = 1; h < E; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < E; i += 2 * h) {
+#pragma unroll
+      for (int j = i; j < i + h; ++j) {
+        const float a = v[j], b = v[j + h];
+        v[j] = a + b;
+        v[j + h] = a - b;
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 5; ++s) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] = fmaf(v[j], sgn[s], __shfl_xor_sync(kFull, v[j], 1 << s));
+  }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);

@@ -75,20 +75,6 @@ struct WinSmem {
   static_assert(4 * kPageTile <= 2 * kQPart, "stages 2 and 3");
 };
 
-// wht_warp of a 128-dim vector with the lanes' signs at hand: one multiply-add per element and
-// cross-lane stage (exact: a product with +-1), where many rows pass through.
-__device__ __forceinline__ void wht_signed(float (&v)[4], const float (&sgn)[5]) {
-  const float a = v[0] + v[1], b = v[0] - v[1], c = v[2] + v[3], d = v[2] - v[3];
-  v[0] = a + c;
-  v[1] = b + d;
-  v[2] = a - c;
-  v[3] = b - d;
-#pragma unroll
-  for (int s = 0; s < 5; ++s)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], sgn[s], __shfl_xor_sync(kFull, v[j], 1 << s));
-}
-
 template <typename TQ, int BITS>
 __global__ void __launch_bounds__(kWThreads, 1)
     window_tc_kernel(const float* __restrict__ params, const uint8_t* __restrict__ blocks,
@@ -153,17 +139,16 @@ __global__ void __launch_bounds__(kWThreads, 1)
     return;
   }
   const int* pt_row = page_table + (size_t)s * max_pages;
-  auto phys_of = [&](int k) {
+  auto entry_of = [&](int k) {  // page-table entry of page k of the chunk, as it is
     const int pg = wp.page(p_begin + k);
-    const int ph = in_bounds(pg < max_pages, status) ? __ldg(pt_row + pg) : -1;
-    return ph >= 0 && ph < n_pages ? ph : -1;
+    return k < n && in_bounds(pg < max_pages, status) ? __ldg(pt_row + pg) : -1;
   };
 
   // ---- tensor memory, barriers, the first two pages ------------------------------------
   if (warp == 12) tc::alloc(tmem_slot, kWCols);
-  auto issue = [&](int k) {  // one thread
-    const int st = k & 1, ph = phys_of(k);
-    if (ph >= 0) {
+  auto issue = [&](int k, int ph) {  // one thread
+    const int st = k & 1;
+    if (ph >= 0 && ph < n_pages) {
       mbar_expect_tx(bars + kRing + st, BB);
       bulk_copy(smem + SM::kOffRing + st * BB, blocks + ((size_t)ph * H + hk) * BB, BB, bars + kRing + st);
     } else {
@@ -179,8 +164,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
                           : i >= kSRead && i < kPvDone ? 128 : 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    issue(0);
-    if (n > 1) issue(1);
+    issue(0, entry_of(0));
+    if (n > 1) issue(1, entry_of(1));
   }
 
   if (tid < 256) row_off[tid] = tid < nh ? row_index(tid) : n_q * n_q_heads;
@@ -215,7 +200,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         for (int i = 0; i < E; ++i) v[j][i] = nx[j][i];
       load(r0 + kWWarps * kAt, nx);
 #pragma unroll
-      for (int j = 0; j < kAt; ++j) wht_signed(v[j], sgn);
+      for (int j = 0; j < kAt; ++j) wht_signed<E>(v[j], sgn);
 #pragma unroll
       for (int j = 0; j < kAt; ++j) {
         const int r = r0 + kWWarps * j;
@@ -270,12 +255,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
     level_tables<BITS>(tl0, tl1, th0, th1);
     const float kf = scale * kLog2e / (ALPHA * (float)D);  // log2 score per (dot * nK)
     int issued = min(n, 2), k = 0;
-    bool page_nx = phys_of(0) >= 0;  // looked up a page ahead
+    // page-table entries of pages k .. k + 2, each loaded three pages ahead of its use
+    int ph0 = entry_of(0), ph1 = entry_of(1), ph2 = entry_of(2);
     for (; k < n; ++k) {
       const int st = k & st_mask;
       const int before = k - st_mask - 1;  // the page that had the stage
       const int ph_before = (before >> st_log) & 1;
       const uint8_t* blk = smem + SM::kOffRing + (k & 1) * BB;
+      const int ph3 = entry_of(k + 3);
       ok = mbar_wait(bars + kRing + (k & 1), (k >> 1) & 1);
       if (k_side) {
         ok = ok && (before < 0 || mbar_wait(bars + kKFree + st, ph_before));
@@ -293,8 +280,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         // nrm[j] = |k_j| kf; nrm[64 + j] = |v_j| / sigma with the CTA's V-norm reference sigma (it
         // only scales the weights), raised when a token some row sees has |v| > kSigmaSlack sigma
         const int tok0 = wp.page(p_begin + k) * kPage;
-        const bool page_ok = page_nx;
-        if (k + 1 < n) page_nx = phys_of(k + 1) >= 0;
+        const bool page_ok = ph0 >= 0 && ph0 < n_pages;
         if (t < 64) {
           if (ok) nrm[st * 128 + t] = half_at(blk + k_norm_off(D, BITS) + 2 * t) * kf;
         } else {
@@ -319,9 +305,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
       if (ring_read()) break;
       if (tid == 256 && k + 2 < n) {
         fence_proxy_async();
-        issue(k + 2);
+        issue(k + 2, ph2);
       }
       if (k + 2 < n) issued = k + 3;
+      ph0 = ph1;
+      ph1 = ph2;
+      ph2 = ph3;
     }
     if (k < n) {  // gave up: wait (bounded) for the copies in flight
       ok = false;
@@ -575,7 +564,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
         if (out != nullptr) {
 #pragma unroll
-          for (int j = 0; j < kAt; ++j) wht_signed(y[j], sgn);
+          for (int j = 0; j < kAt; ++j) wht_signed<E>(y[j], sgn);
         }
 #pragma unroll
         for (int j = 0; j < kAt; ++j) {
