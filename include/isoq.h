@@ -71,6 +71,9 @@ extern "C" {
  * rotating the block y_b (read as the quaternion w + x i + y j + z k, Hamilton
  * convention) to z_b = p_b * y_b * conj(q_b).  That is d/4 * 8 = 256 stored parameters
  * per head at d = 128 (the paper's count, versus d^2 = 16,384 for a dense rotation).
+ * (A handle also keeps derived device copies: the blocks as matrices, 4 d floats per head,
+ * and for the read-back the dense inverse rotation in two binary16 parts, 4 d^2 bytes per
+ * head.)
  * K and V of one KV head share the same parameters.
  *
  * Values are drawn from SplitMix64 (Steele, Lea & Flood, OOPSLA 2014) seeded with `seed`:
@@ -281,7 +284,10 @@ int isoq_quantize_append_layers(const isoq_params* const* params,
  * ISOQ_ST_SEQ_RANGE / _POS_RANGE / _PAGE_RANGE: its rows of K and V stay as they were.  A
  * slot that was never appended reads as whatever its bytes stand for.  rope_table: device,
  * 16-byte aligned, as for isoq_quantize_append_rope.  n_tokens == 0 is a no-op.
- * Arithmetic: the levels and the rotation in binary32.
+ * Arithmetic: sums in binary32.  To fp32, and for short lists, the levels and the rotation are
+ * binary32 as well; from 2^20 elements on, 16-bit outputs take the levels as binary16 (relative
+ * error < 6e-5) and the rotation as binary16, in two parts for fp16 (22 bits), in one for bf16
+ * (11 bits: ~1.5e-4 of the vector's rms, a tenth of what rounding to bf16 costs).
  * Errors: ISOQ_E_ARG, ISOQ_E_DIM, ISOQ_E_DEVICE, ISOQ_E_CUDA.
  * ===================================================================================== */
 int isoq_dequantize(const isoq_params* params, const isoq_cache* cache, const int32_t* seq_ids,

@@ -776,7 +776,7 @@ size_t isoq_window_workspace_bytes(int n_seqs, int n_q, int n_q_heads, int n_kv_
   if (n_seqs < 0 || n_q < 1 || n_q_heads < 0 || n_kv_heads < 1 || max_seq_len < 0 || window < 1 ||
       n_sinks < 0)
     return 0;
-  if (!supported_d(d) || n_q_heads % n_kv_heads) return 0;
+  if (!supported_d(d) || n_q_heads % n_kv_heads || !rows_fit(n_q, n_q_heads, n_kv_heads)) return 0;
   const int ns = plan_window(n_seqs, n_q_heads, n_kv_heads, d, max_seq_len, n_q, window, n_sinks)
                      .n_splits;
   return (size_t)n_seqs * n_q * n_q_heads * ns * isoq::partial_stride(d) * sizeof(float);

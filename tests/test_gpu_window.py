@@ -182,6 +182,88 @@ def test_chunk_window(oracle, i):
     c.check(oracle, c.run())
 
 
+@pytest.mark.parametrize("n_q,hq,hkv,d", [(1, 8, 2, 128), (1, 4, 2, 256), (3, 8, 2, 128), (40, 8, 2, 128), (200, 8, 2, 128),
+                                         (9, 4, 2, 256)])
+def test_empty_sequences_give_zeros(n_q, hq, hkv, d):
+    c = _case(1, lens=[0, 0, 0], hq=hq, hkv=hkv, W=5, S=2, n_q=n_q, d=d)
+    assert c.max_len == 0 and bool((c.run() == 0).all())
+    c.max_len, c.W = 10 ** 6, 10 ** 6      # a plan of many chunks, all of them empty
+    assert bool((c.run() == 0).all()) and iq.isoq_get_status(c.cache) == 0
+
+
+def test_a_long_chunk_at_d256(oracle):
+    c = _case(2, lens=[700, 150], hq=4, hkv=2, W=120, S=3, n_q=150, d=256)
+    c.check(oracle, c.run())
+
+
+def test_sequences_that_share_pages(oracle):
+    """A shared prefix: three sequences whose first pages are the same physical pages."""
+    c = _case(3, lens=[500, 500, 500], hq=8, hkv=2, W=200, S=64, poison=False)
+    c.pt[1:, :5] = c.pt[0, :5]
+    c.cache.page_table.copy_(c.pt)
+    c.check(oracle, c.run())
+
+
+def test_two_streams_at_once():
+    a = _case(4, lens=[3000, 2000], hq=32, hkv=4, W=1500, S=4)
+    b = _case(5, lens=[900, 1000], hq=64, hkv=8, W=700, S=64, n_q=40)
+    want = a.run(), b.run()
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    ws, out = (a.workspace(), b.workspace()), (torch.empty_like(want[0]), torch.empty_like(want[1]))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(sa):
+            a.run(ws=ws[0], out=out[0])
+        with torch.cuda.stream(sb):
+            b.run(ws=ws[1], out=out[1])
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+FIRST_CAPTURED = """
+import torch, rotated_bit_kv_isoquant_b200 as iq
+d, H, L = 128, 2, 1500
+p = iq.isoq_make_params(0, d, H)
+c = iq.PagedCache(d, H, 24, torch.arange(24)[None])
+x = torch.randn(L, H, d, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).bfloat16()
+sid, pos = torch.zeros(L, dtype=torch.int32, device="cuda"), torch.arange(L, dtype=torch.int32, device="cuda")
+iq.isoq_quantize_append(p, c, x, x, sid, pos)
+lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+for n_q in (1, 4, 50):
+    Q = torch.randn(1, n_q, 8, d, device="cuda")
+    out, again = torch.zeros(2, 1, n_q, 8, d, device="cuda")
+    ws = torch.empty(max(16, iq.isoq_window_workspace_bytes(1, n_q, 8, H, d, L, 700, 4)), dtype=torch.uint8, device="cuda")
+    run = lambda o: iq.isoq_multi_token_attention_window(p, c, Q, lens, L, 700, 4, o, 0.1, ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(out)
+    g.replay()
+    run(again)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again) and bool(out.any()), n_q
+K = torch.zeros(L, H, d, dtype=torch.bfloat16, device="cuda")
+for n in (5, L):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        iq.isoq_dequantize(p, c, sid[:n], pos[:n], K[:n], None)
+    g.replay()
+    torch.cuda.synchronize()
+    assert bool(K[n - 1].any())
+assert iq.isoq_get_status(c) == 0
+print("ok")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST_CAPTURED], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr[-2000:]
+
+
 def test_one_token_chunk_is_the_decode(oracle):
     c = _case(3, lens=[500, 90], hq=8, hkv=2, W=100, S=4)
     a, b = c.run(chunk=False), c.run(chunk=True)

@@ -65,7 +65,8 @@ def test_workspace_refuses():
     for bad in [(-1, 1, 8, 2, 128, 1000, 100, 4), (1, 0, 8, 2, 128, 1000, 100, 4),
                 (1, 1, 7, 2, 128, 1000, 100, 4), (1, 1, 8, 0, 128, 1000, 100, 4),
                 (1, 1, 8, 2, 96, 1000, 100, 4), (1, 1, 8, 2, 128, -1, 100, 4),
-                (1, 1, 8, 2, 128, 1000, 0, 4), (1, 1, 8, 2, 128, 1000, 100, -1)]:
+                (1, 1, 8, 2, 128, 1000, 0, 4), (1, 1, 8, 2, 128, 1000, 100, -1),
+                (1, 2 ** 31 - 1, 8, 2, 128, 1000, 100, 4)]:
         assert f(*bad) == 0, bad
 
 
@@ -89,6 +90,9 @@ def test_binding_checks_shapes_and_devices():
                        (Q[..., :64], lens, Q[..., :64]), (Q, lens.to("meta"), Q)]:
         with pytest.raises(ValueError):
             call(None, _Cache, q, sl, 100, 16, 4, out, 1.0, ws)
+    for W, S in [(0, 4), (2 ** 31, 4), (2 ** 32 + 16, 4), (16, -1), (16, 2 ** 31)]:
+        with pytest.raises(ValueError):
+            call(None, _Cache, Q, lens, 100, W, S, Q, 1.0, ws)
     with pytest.raises(ValueError):
         iq.isoq_multi_token_attention_window(None, _Cache, Q, lens, 100, 16, 4, Q, 1.0, ws)
 
