@@ -294,10 +294,17 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
   }
   __syncwarp();
   const int* pt_row = page_table + (size_t)s * max_pages;
-  // task k of this warp: page slot p_begin + (warp + NW * k) / SUB, its SUB-th part
-  const int n_my = (SUB * (p_end - p_begin) - warp + NW - 1) / NW;  // may be <= 0
+  // task k of this warp: page slot p_begin + (warp + NW * k) / SUB, its SUB-th part (with one
+  // task a page written without the division: otherwise the compiler lays the whole kernel out
+  // differently, and the unwindowed decode of 8 x 131072 tokens takes 1.4% longer)
+  const int n_my = (SUB == 1 ? p_end - p_begin - warp + NW - 1
+                             : SUB * (p_end - p_begin) - warp + NW - 1) / NW;  // may be <= 0
+  auto page_of = [&](int k) {
+    if constexpr (SUB == 1) return wp.page(p_begin + warp + NW * k);
+    else return wp.page(p_begin + (warp + NW * k) / SUB);
+  };
   auto issue = [&](int k) {  // lane 0 only
-    const int pg = wp.page(p_begin + (warp + NW * k) / SUB);
+    const int pg = page_of(k);
     const int st = k % NST;
     const int phys = in_bounds(pg < max_pages && st < NST, status) ? __ldg(pt_row + pg) : -1;
     if (phys >= 0 && phys < n_pages && in_bounds(hk < H, status)) {
@@ -438,7 +445,7 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
       break;
     }
     const uint8_t* blk = myring + st * BB;
-    const int pg = wp.page(p_begin + (warp + NW * k) / SUB);
+    const int pg = page_of(k);
     const int phys = in_bounds(pg < max_pages && st < NST, status) ? __ldg(pt_row + pg) : -1;
     const bool page_ok = phys >= 0 && phys < n_pages;
     const int tok0 = pg * kPage;

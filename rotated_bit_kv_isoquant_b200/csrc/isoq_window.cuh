@@ -75,9 +75,8 @@ __device__ __forceinline__ bool win_sees(const WinArgs& w, int lo, int t) {
 template <bool WIN>
 __device__ __forceinline__ int clamp_len(int len, int max_pages, const WinArgs& w, bool report,
                                          uint32_t* status) {
-  const long long cap = (long long)max_pages * kPage;
-  const int most = WIN ? (int)min((long long)w.max_len, cap)
-                       : (int)min(cap, (long long)0x7fffffff);
+  int most = max_pages * kPage;
+  if constexpr (WIN) most = (int)min((long long)w.max_len, (long long)max_pages * kPage);
   if (len > most) {
     if (report) set_status(status, ISOQ_ST_LEN_RANGE);
     len = most;
