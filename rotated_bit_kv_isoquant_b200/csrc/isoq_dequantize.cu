@@ -41,8 +41,9 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[E]) {
 // dims l E .. l E + E-1 and the head's blocks of them.  The run's pages are looked up at once, a
 // token a lane, and the next token's words are loaded while one is computed.  The shuffles of
 // the WHT bound it (20 a vector at d = 128, with the loads ~30 of the load-store pipe's cycles):
-// 32768 tokens x 8 heads to fp32 in 188 us with a token a warp, which the lookups bounded, 158
-// with four heads of a token a warp, whose blocks were loaded again for each.
+// 32768 tokens x 8 heads to fp32 in 111 us (2.7 TB/s), at d = 256 in 199 (3.0 TB/s); 188 with a
+// token a warp, which the lookups bounded, 158 with four heads of a token a warp, whose blocks
+// were loaded again for each.
 constexpr int kDqWarps = 8;
 struct HeadWords {  // what a lane needs of a token's K and V codes, and the norms
   uint32_t k[3], v[3];
@@ -51,7 +52,7 @@ struct HeadWords {  // what a lane needs of a token's K and V codes, and the nor
   bool live;
 };
 
-template <int D, int BITS, typename T>
+template <int D, int BITS, typename T, bool ROPE>
 __global__ void __launch_bounds__(kDqWarps * 32) dequantize_warp_kernel(const DequantizeArgs a, int tokens) {
   constexpr int E = D / 32, NB = E / 4, CB = code_bytes(D, BITS), BB = block_bytes(D, BITS);
   __shared__ float level[16];  // by the stored field: the code, or the 4-bit sign-magnitude
@@ -146,13 +147,15 @@ __global__ void __launch_bounds__(kDqWarps * 32) dequantize_warp_kernel(const De
       const float c = n * (1.0f / D);
 #pragma unroll
       for (int e = 0; e < E; ++e) y[e] *= c;
-      if (a.rope && side == 0) {  // lanes 0-15 hold the first halves of the pairs
-        const float* cs = a.rope + ((size_t)pos * (D / 2) + (lane & 15) * E) * 2;
+      if (ROPE && side == 0) {  // lanes 0-15 hold the first halves of the pairs
+        const float4* cs = reinterpret_cast<const float4*>(
+            a.rope + ((size_t)pos * (D / 2) + (lane & 15) * E) * 2);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float other = __shfl_xor_sync(kFull, y[e], 16);
-          const float2 r = __ldg(reinterpret_cast<const float2*>(cs) + e);
-          y[e] = fmaf(lane < 16 ? other : -other, r.y, y[e] * r.x);
+        for (int e = 0; e < E; e += 2) {
+          const float4 r = __ldg(cs + e / 2);  // (cos, sin) of two pairs
+          const float p0 = __shfl_xor_sync(kFull, y[e], 16), p1 = __shfl_xor_sync(kFull, y[e + 1], 16);
+          y[e] = fmaf(lane < 16 ? p0 : -p0, r.y, y[e] * r.x);
+          y[e + 1] = fmaf(lane < 16 ? p1 : -p1, r.w, y[e + 1] * r.z);
         }
       }
       store_vec<T, E>(out + ((size_t)(i0 + t) * a.n_kv_heads + h) * D + dim, y);
@@ -168,7 +171,8 @@ cudaError_t launch_warp(const DequantizeArgs& a, cudaStream_t stream, int n_sm) 
   tokens = tokens < 1 ? 1 : tokens > 16 ? 16 : tokens;
   const long long per_cta = tokens * kDqWarps;
   dim3 grid((unsigned)((a.n_tokens + per_cta - 1) / per_cta), a.n_kv_heads);
-  dequantize_warp_kernel<D, BITS, T><<<grid, kDqWarps * 32, 0, stream>>>(a, (int)tokens);
+  if (a.rope) dequantize_warp_kernel<D, BITS, T, true><<<grid, kDqWarps * 32, 0, stream>>>(a, (int)tokens);
+  else dequantize_warp_kernel<D, BITS, T, false><<<grid, kDqWarps * 32, 0, stream>>>(a, (int)tokens);
   return cudaGetLastError();
 }
 

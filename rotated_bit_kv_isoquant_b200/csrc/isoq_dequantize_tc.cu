@@ -20,16 +20,16 @@
 // reads the V tile layout's groups as they are, four tokens at a time; other tokens pick
 // their own nibbles out of the groups.
 //
-// Measured (32768 consecutive tokens, 8 KV heads, K and V): d = 128 to bf16 45 us (3.55 TB/s
-// of codes read and values written; the warp-per-token kernel: 162 us), to fp16 55 us, with
-// the rotary embedding 74 and 109 us; d = 256 to bf16 148 us.  ncu on the first: DRAM 28%,
-// issue 59% of the cycles, tensor pipe ~16%: bound by the instructions of the fill and the
-// write-out (45 a vector) and by the chain of one tile's steps.  Tried: the output staged in
-// shared memory and sent as one bulk copy a row, 57-70 us (the copy engine takes ~33 cycles
-// a row) or written by 16 lanes a row, 57 us; each thread writing its own row's columns, 56 us
-// (32 lines an instruction); the page lookups not pipelined, 70 us; twice the threads a CTA,
-// 61 us.  The accumulator is therefore read as 16-row fragments whose columns are ordered so
-// that a quad writes 128 contiguous bytes.
+// Measured (32768 consecutive tokens, 8 KV heads, K and V): d = 128 to bf16 45 us (3.6 TB/s of
+// codes read and values written), to fp16 53 us, with the rotary embedding 74 and 109 us;
+// d = 256 to bf16 139 us, with the embedding 234.  ncu on the first: ALU pipe 57% busy, issue
+// 56% of the cycles, DRAM 28%, tensor pipe 20%: bound by the instructions of the fill and the
+// write-out (44 a vector) and by the chain of one tile's steps.  Tried, the first in us: the
+// output staged in shared memory and sent as one bulk copy a row, 57-70 (the copy engine takes
+// ~33 cycles a row), or written by 16 lanes a row, 57; each thread writing its own row's
+// columns, 56 (32 lines an instruction); the page lookups not pipelined, 70; twice the threads
+// a CTA, 61.  The accumulator is therefore read as 16-row fragments whose columns are ordered
+// so that a quad writes 128 contiguous bytes.
 #include "isoq_check.cuh"
 #include "isoq_common.cuh"
 #include "isoq_dequantize.cuh"
@@ -61,11 +61,9 @@ struct ReadSmem {
   static constexpr int kOffWhole = kOffNorm + 3 * kTile * 4;  // int [3][8]: 16-row blocks in order
   static constexpr int kOffBar = kOffWhole + 3 * 8 * 4;
   static constexpr int kOffTmem = kOffBar + 2 * 8;
-  // the rotary table's 64 pairs of the tile's 64 keys, 512 bytes a row; the widest form has no
-  // room for them and reads the table where it lies
-  static constexpr bool kTable = ROPE && !(D == 256 && LO);
+  // the rotary table's 64 pairs of the tile's 64 keys, 512 bytes a row
   static constexpr int kOffTable = (kOffTmem + 16 + 127) / 128 * 128;
-  static constexpr int kBytes = kTable ? kOffTable + 64 * 512 : kOffTmem + 16;
+  static constexpr int kBytes = ROPE ? kOffTable + 64 * 512 : kOffTmem + 16;
   static_assert(kBytes <= 227 * 1024, "shared memory");
   static_assert(kOffA % 1024 == 0 && kOffBar % 8 == 0 && kOffRow % 16 == 0, "alignment");
 };
@@ -331,7 +329,7 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
       __syncwarp();
     }
     pending = true;
-    if constexpr (SM::kTable) {  // the table's rows of this tile, while the product runs
+    if constexpr (ROPE) {  // the table's rows of this tile, while the product runs
 #pragma unroll
       for (int x = tid; x < 64 * 32; x += NT) {
         const int r = x >> 5, c = x & 31;  // 16-byte chunk c (two pairs) of row r
@@ -348,7 +346,7 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
 
     // ---- the product's rows: scale, rotary embedding, round, out --------------------------
     ok = __all_sync(kFull, mbar_wait(bars + 1, k & 1));  // warp-uniform: collective loads
-    if constexpr (SM::kTable) {
+    if constexpr (ROPE) {
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();
     }
@@ -377,12 +375,8 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
           if constexpr (ROPE) {
             if (!my_side) {
               // (cos, sin) of the pairs my_dim + 2 i, + 1: a cos + b sin, or b cos - a sin
-              float4 t;
-              if constexpr (SM::kTable)
-                t = *reinterpret_cast<const float4*>(smem + SM::kOffTable + table_at(row, 8 * (lane & 3) + i));
-              else
-                t = __ldg(reinterpret_cast<const float4*>(
-                              a.rope + ((size_t)r.pos * (D / 2) + my_dim) * 2) + i);
+              const float4 t =
+                  *reinterpret_cast<const float4*>(smem + SM::kOffTable + table_at(row, 8 * (lane & 3) + i));
               const float s0 = hf ? -t.y : t.y, s1 = hf ? -t.w : t.w;
               y = make_float2(fmaf(__uint_as_float(u[4 * i + 2 * e]), s0, y.x * t.x),
                               fmaf(__uint_as_float(u[4 * i + 2 * e + 1]), s1, y.y * t.z));
@@ -441,19 +435,24 @@ cudaError_t launch_tc_t(const DequantizeArgs& a, cudaStream_t stream, int n_sm) 
   if (a.dtype == ISOQ_BF16)
     return a.rope ? launch_tc<D, BITS, __nv_bfloat16, false, true>(a, stream, n_sm)
                   : launch_tc<D, BITS, __nv_bfloat16, false, false>(a, stream, n_sm);
-  return a.rope ? launch_tc<D, BITS, __half, true, true>(a, stream, n_sm)
-                : launch_tc<D, BITS, __half, true, false>(a, stream, n_sm);
+  if constexpr (D == 128) {
+    if (a.rope) return launch_tc<D, BITS, __half, true, true>(a, stream, n_sm);
+  }
+  return launch_tc<D, BITS, __half, true, false>(a, stream, n_sm);
 }
 
 }  // namespace
 
 // From 2^20 elements on (8192 vectors of 128, 4096 of 256): below, loading R and the chain of
 // one tile cost more than the warp kernel's shuffles.  Measured, bf16, 8 KV heads, d = 128 /
-// 256, us a call (this kernel | the warp kernel): 256 tokens 4.8 | 3.9 / 5.7 | 6.1, 512 tokens
-// 4.9 | 5.1 / 5.9 | 9.2, 4096 tokens 8.9 | 23.3 / 22.7 | 53.5.
+// 256, us a call (this kernel | the warp kernel): 256 tokens 4.8 | 3.8 / 5.7 | 6.0, 512 tokens
+// 4.9 | 5.2 / 5.9 | 10.7, 4096 tokens 9.0 | 18 / 22 | 33.  fp16 with the rotary embedding at d =
+// 256 stays with the warp kernel: both parts of R leave no room for the staged table, and
+// reading it in place took 330 us for 32768 tokens against 280.
 bool use_dequantize_tc(const DequantizeArgs& a) {
   const long long vectors = (long long)a.n_tokens * a.n_kv_heads * ((a.K != nullptr) + (a.V != nullptr));
-  return a.dtype != ISOQ_F32 && vectors * a.d >= (1ll << 20);
+  if (a.dtype == ISOQ_F32 || (a.dtype == ISOQ_F16 && a.d == 256 && a.rope)) return false;
+  return vectors * a.d >= (1ll << 20);
 }
 
 cudaError_t launch_dequantize_tc(const DequantizeArgs& a, cudaStream_t stream, int n_sm) {
