@@ -22,6 +22,15 @@
 // accumulators, statistics are f32 (as in the multi-token kernel, whose error bounds hold).
 // A call whose rows' pages fit one chunk divides, rotates back and writes its output here.
 // Otherwise partial states go to the combine.
+//
+// Measured (64 query / 8 KV heads, window 4096): 2048 query tokens of one sequence 532 us (517
+// TFLOP/s of scores and values, the low query part not counted), 16 tokens of 8 sequences 70 us.
+// A page of 256 rows takes ~3800 cycles, of which a softmax warp computes ~2500: its latency
+// bounds the kernel (issue 49% of the cycles, tensor pipe 37%, exponent unit 26%).  Why this
+// split: one CTA of 128 threads doing the steps in turn, two per SM, took 1266 us; the score
+// products read A and B from shared memory (48 cycles of its bandwidth for 32 of the tensor
+// core), so 256 rows share a page's tiles, and the next page's scores are issued before this
+// page's value products.
 #include <math_constants.h>
 
 #include <type_traits>

@@ -235,10 +235,11 @@ def test_keys_moved_to_other_positions(oracle):
                                 d ** -0.5, W, S)
     assert (np.linalg.norm(out[:, None].cpu().numpy() - ref, axis=-1) <= tol).all()
     # the codes survive the move: V, which has no rotary embedding, is coded as it was
+    v_codes = slice(64 * (48 + 2), 64 * (48 + 2 + 48))  # of a block at d = 128, 3 bits
     oldc = oracle.unpack_codes_batch(oracle.v_region_records(np.ascontiguousarray(
-        s.cache.blocks.cpu().numpy()[..., 3200:3200 + 3072]), d), d)
+        s.cache.blocks.cpu().numpy()[..., v_codes]), d), d)
     newc = oracle.unpack_codes_batch(oracle.v_region_records(np.ascontiguousarray(
-        cache.blocks.cpu().numpy()[..., 3200:3200 + 3072]), d), d)
+        cache.blocks.cpu().numpy()[..., v_codes]), d), d)
     old = oldc[s.pt[0, s.pos[at] // 64].numpy(), :, s.pos[at].numpy() % 64]
     new = newc[pt[0].numpy()[np.arange(n) // 64], :, np.arange(n) % 64]
     assert np.array_equal(old, new)
