@@ -159,7 +159,9 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
   auto put_row = [&](int st) {
     if (tid < kTile) {
       const bool ok = pg >= 0 && pg < a.n_pages;
-      if (!ok && pg_bad && h == 0 && q == 0 && (!both || tid < 64)) set_status(a.status, pg_bad);
+      // one report a token: with both sides in the tile, of the K row, or of the V row without K
+      const bool mine = !both || (tid < 64) == (a.K != nullptr);
+      if (!ok && pg_bad && h == 0 && q == 0 && mine) set_status(a.status, pg_bad);
       TileRow r;
       r.blk = ok ? a.blocks + ((size_t)pg * a.n_kv_heads + h) * BB : nullptr;
       r.pos = pg_p;
