@@ -30,8 +30,11 @@ namespace {
 
 thread_local int g_last_cuda_error = 0;
 
+// The call's error by its return value alone: the runtime keeps a refused call's error as the
+// thread's last one, where the caller's next check of its own launches would find it.
 int cuda_fail(cudaError_t e) {
   g_last_cuda_error = (int)e;
+  cudaGetLastError();
   return ISOQ_E_CUDA;
 }
 
