@@ -387,7 +387,8 @@ int isoq_decode_attention_noalloc(const isoq_params* params, const isoq_cache* c
  * [n_seqs][n_q][n_q_heads][d].  workspace: device, 16-byte aligned, at least
  * isoq_multi_token_workspace_bytes(...) bytes for the same sizes.  Other arguments as
  * isoq_decode_attention; n_q = 1 is exactly the decode.  Requires
- * n_kv_heads * ceil(n_q * n_q_heads / n_kv_heads / 8) <= 65535, else ISOQ_E_ARG.
+ * n_kv_heads * ceil(n_q * n_q_heads / n_kv_heads / 8) <= 65535 (at d = 256, where the kernel
+ * takes 4 rows at a time, / 4), else ISOQ_E_ARG.
  * Errors: ISOQ_E_ARG, ISOQ_E_DIM, ISOQ_E_GQA, ISOQ_E_WORKSPACE, ISOQ_E_DEVICE, ISOQ_E_CUDA.
  * ===================================================================================== */
 size_t isoq_multi_token_workspace_bytes(int n_seqs, int n_q, int n_q_heads, int n_kv_heads,

@@ -645,10 +645,12 @@ size_t isoq_decode_workspace_bytes(int n_seqs, int n_q_heads, int n_kv_heads, in
 
 namespace {
 
-// The split kernel's grid.y = n_kv_heads * ceil(n_q * group / 8) must stay <= 65535.
-bool rows_fit(int n_q, int n_q_heads, int n_kv_heads) {
+// The split kernels' grid.y = n_kv_heads * (blocks of a KV head's rows) must stay <= 65535: blocks
+// of 4 rows at d = 256, of at least 8 (one block, if they are at most 4) at d = 128.
+bool rows_fit(int n_q, int n_q_heads, int n_kv_heads, int d) {
   const long long group = n_kv_heads > 0 ? n_q_heads / n_kv_heads : 0;
-  return (long long)n_kv_heads * (((long long)n_q * group + 7) / 8) <= 65535;
+  const int block = isoq::decode_rows_per_block(d, n_q, (int)group);
+  return (long long)n_kv_heads * (((long long)n_q * group + block - 1) / block) <= 65535;
 }
 
 // Shared by the decode entry points: validation, the split plan, then the split kernel and
@@ -664,7 +666,7 @@ int decode_common_impl(const isoq_params* params, const isoq_cache* cache, const
   if (!(scale == scale) || isinf(scale)) return ISOQ_E_ARG;
   if (n_q_heads % cache->n_kv_heads || n_q_heads / cache->n_kv_heads > 16) return ISOQ_E_GQA;
   if (n_seqs > cache->n_seqs) return ISOQ_E_ARG;
-  if (n_q < 1 || !rows_fit(n_q, n_q_heads, cache->n_kv_heads)) return ISOQ_E_ARG;
+  if (n_q < 1 || !rows_fit(n_q, n_q_heads, cache->n_kv_heads, cache->d)) return ISOQ_E_ARG;
   if (n_seqs == 0 || n_q_heads == 0) return ISOQ_OK;
   if (!Q || !seq_lens || !(out || state) || !workspace) return ISOQ_E_ARG;
   if (state && ((uintptr_t)state & 15u) != 0) return ISOQ_E_ARG;
@@ -779,7 +781,7 @@ size_t isoq_window_workspace_bytes(int n_seqs, int n_q, int n_q_heads, int n_kv_
   if (n_seqs < 0 || n_q < 1 || n_q_heads < 0 || n_kv_heads < 1 || max_seq_len < 0 || window < 1 ||
       n_sinks < 0)
     return 0;
-  if (!supported_d(d) || n_q_heads % n_kv_heads || !rows_fit(n_q, n_q_heads, n_kv_heads)) return 0;
+  if (!supported_d(d) || n_q_heads % n_kv_heads || !rows_fit(n_q, n_q_heads, n_kv_heads, d)) return 0;
   const int ns = plan_window(n_seqs, n_q_heads, n_kv_heads, d, max_seq_len, n_q, window, n_sinks)
                      .n_splits;
   return (size_t)n_seqs * n_q * n_q_heads * ns * isoq::partial_stride(d) * sizeof(float);

@@ -1,0 +1,39 @@
+"""The windowed calls at the ends of what they accept: sizes at the grid's limits, a workspace of
+exactly the size asked for, and lengths next to the largest position."""
+import numpy as np
+import pytest
+import torch
+
+import rotated_bit_kv_isoquant_b200 as iq
+from test_gpu_window import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+
+
+def _raw(c, Q, out, ws, n_q, window=True):
+    lib, st = iq.raw_lib(), torch.cuda.current_stream().cuda_stream
+    if not window:
+        return lib.isoq_multi_token_attention(c.params.handle, c.cache.c, Q.data_ptr(), iq.ISOQ_BF16, Q.shape[0], n_q,
+                                              Q.shape[-2], c.sl.data_ptr(), c.max_len, out.data_ptr(), 0.1,
+                                              ws.data_ptr(), ws.numel(), st)
+    return lib.isoq_multi_token_attention_window(c.params.handle, c.cache.c, Q.data_ptr(), iq.ISOQ_BF16, Q.shape[0],
+                                                 n_q, Q.shape[-2], c.sl.data_ptr(), c.max_len, c.W, c.S,
+                                                 out.data_ptr(), iq.ISOQ_F32, 0.1, ws.data_ptr(), ws.numel(), st)
+
+
+def test_the_longest_chunk_at_d256(oracle):
+    """65520 row blocks of 4 fit the grid and are right; one token more is refused, not launched."""
+    c = Case([300], 16, 8, 64, 4, n_q=16380, d=256, out="f32", poison=False)
+    out = c.run()
+    c.Q, out = c.Q[:, -40:].contiguous(), out[:, -40:]
+    c.check(oracle, out)
+    Q = torch.zeros((1, 16384, 16, 256), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")
+    for window in (True, False):
+        assert _raw(c, Q, out, ws, 16384, window) == iq.ISOQ_E_ARG

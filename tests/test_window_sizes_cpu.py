@@ -1,0 +1,18 @@
+"""Sizes that the windowed calls refuse have no workspace size, and the binding's numbers keep
+their value on the way into the C interface's ints."""
+import pytest
+import torch
+
+import rotated_bit_kv_isoquant_b200 as iq
+from test_window_cpu import _Cache
+
+f = iq.raw_lib().isoq_window_workspace_bytes
+
+
+@pytest.mark.parametrize("hq,hkv,fits", [(64, 8, 4095), (16, 16, 4 * 4095), (8, 2, 32767), (32, 2, 2 * 4095)])
+def test_rows_at_d256_are_counted_in_blocks_of_four(hq, hkv, fits):
+    """d = 256 works on blocks of 4 rows: at most 65535 of them over the KV heads."""
+    assert hkv * -(-fits * (hq // hkv) // 4) <= 65535 < hkv * -(-(fits + 4) * (hq // hkv) // 4)
+    assert f(1, fits, hq, hkv, 256, 1000, 100, 4) > 0
+    assert f(1, fits + 4, hq, hkv, 256, 1000, 100, 4) == 0
+    assert f(1, fits + 4, hq, hkv, 128, 1000, 100, 4) > 0      # blocks of 8 and more
