@@ -331,6 +331,7 @@ int isoq_dequantize_rope(const isoq_params* params, const isoq_cache* cache,
  * isoq_decode_workspace_bytes.  out: device fp32 [n_seqs][n_q_heads][d].
  * workspace: device, at least isoq_decode_workspace_bytes(...) bytes, 16-byte aligned,
  * contents need not be initialised.  Calls that share a workspace must not overlap.
+ * n_seqs <= 65535, in this and the other attention calls, else ISOQ_E_ARG.
  * Errors: ISOQ_E_ARG, ISOQ_E_DIM, ISOQ_E_GQA, ISOQ_E_WORKSPACE, ISOQ_E_CUDA.
  * ===================================================================================== */
 size_t isoq_decode_workspace_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int d,

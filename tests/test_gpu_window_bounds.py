@@ -37,3 +37,30 @@ def test_the_longest_chunk_at_d256(oracle):
     ws = torch.empty(16, dtype=torch.uint8, device="cuda")
     for window in (True, False):
         assert _raw(c, Q, out, ws, 16384, window) == iq.ISOQ_E_ARG
+
+
+def test_more_sequences_than_a_grid_holds_are_refused():
+    n = 65536
+    params = iq.isoq_make_params(0, 128, 1)
+    cache = iq.PagedCache(128, 1, 1, torch.zeros((n, 1), dtype=torch.int32))
+    x = torch.randn((3, 1, 128), device="cuda")
+    i = torch.arange(3, dtype=torch.int32, device="cuda")
+    iq.isoq_quantize_append(params, cache, x, x, torch.zeros_like(i), i)
+    Q, out = torch.randn((n, 1, 128), device="cuda"), torch.full((n, 1, 128), 3.0, device="cuda")
+    lens = torch.full((n,), 3, dtype=torch.int32, device="cuda")
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+
+    def calls(m):
+        yield lambda: iq.isoq_decode_attention_window(params, cache, Q[:m], lens[:m], 3, 8, 0, out[:m], 0.1, ws)
+        yield lambda: iq.isoq_decode_attention(params, cache, Q[:m], lens[:m], 3, out[:m], 0.1, ws)
+    for call in calls(n):
+        with pytest.raises(iq.IsoqError) as e:
+            call()
+        assert e.value.code == iq.ISOQ_E_ARG
+    torch.cuda.synchronize()
+    assert bool((out == 3.0).all())
+    for call in calls(n - 1):
+        out.fill_(3.0)
+        call()
+        assert bool((out[:-1] != 3.0).any(-1).all()) and bool((out[-1] == 3.0).all())
+    assert iq.isoq_get_status(cache) == 0

@@ -16,3 +16,8 @@ def test_rows_at_d256_are_counted_in_blocks_of_four(hq, hkv, fits):
     assert f(1, fits, hq, hkv, 256, 1000, 100, 4) > 0
     assert f(1, fits + 4, hq, hkv, 256, 1000, 100, 4) == 0
     assert f(1, fits + 4, hq, hkv, 128, 1000, 100, 4) > 0      # blocks of 8 and more
+
+
+def test_more_sequences_than_a_grid_holds():
+    assert f(65535, 1, 8, 2, 128, 1000, 100, 4) > 0
+    assert f(65536, 1, 8, 2, 128, 1000, 100, 4) == 0
