@@ -652,6 +652,10 @@ bool rows_fit(int n_q, int n_q_heads, int n_kv_heads, int d) {
   const int block = isoq::decode_rows_per_block(d, n_q, (int)group);
   return (long long)n_kv_heads * (((long long)n_q * group + block - 1) / block) <= 65535;
 }
+// Whole groups of at most 16 query heads per KV head.
+bool valid_gqa(int n_q_heads, int n_kv_heads) {
+  return n_q_heads % n_kv_heads == 0 && n_q_heads / n_kv_heads <= 16;
+}
 constexpr int kMaxSeqs = 65535;  // their grid.z, and the combine's grid.y
 
 // Shared by the decode entry points: validation, the split plan, then the split kernel and
@@ -665,7 +669,7 @@ int decode_common_impl(const isoq_params* params, const isoq_cache* cache, const
   if (rc) return rc;
   if (n_seqs < 0 || n_q_heads < 0 || max_seq_len < 0 || !valid_dtype(q_dtype)) return ISOQ_E_ARG;
   if (!(scale == scale) || isinf(scale)) return ISOQ_E_ARG;
-  if (n_q_heads % cache->n_kv_heads || n_q_heads / cache->n_kv_heads > 16) return ISOQ_E_GQA;
+  if (!valid_gqa(n_q_heads, cache->n_kv_heads)) return ISOQ_E_GQA;
   if (n_seqs > cache->n_seqs || n_seqs > kMaxSeqs) return ISOQ_E_ARG;
   if (n_q < 1 || !rows_fit(n_q, n_q_heads, cache->n_kv_heads, cache->d)) return ISOQ_E_ARG;
   if (n_seqs == 0 || n_q_heads == 0) return ISOQ_OK;
@@ -782,7 +786,8 @@ size_t isoq_window_workspace_bytes(int n_seqs, int n_q, int n_q_heads, int n_kv_
   if (n_seqs < 0 || n_seqs > kMaxSeqs || n_q < 1 || n_q_heads < 0 || n_kv_heads < 1 ||
       max_seq_len < 0 || window < 1 || n_sinks < 0)
     return 0;
-  if (!supported_d(d) || n_q_heads % n_kv_heads || !rows_fit(n_q, n_q_heads, n_kv_heads, d)) return 0;
+  if (!supported_d(d) || !valid_gqa(n_q_heads, n_kv_heads) || !rows_fit(n_q, n_q_heads, n_kv_heads, d))
+    return 0;
   const int ns = plan_window(n_seqs, n_q_heads, n_kv_heads, d, max_seq_len, n_q, window, n_sinks)
                      .n_splits;
   return (size_t)n_seqs * n_q * n_q_heads * ns * isoq::partial_stride(d) * sizeof(float);

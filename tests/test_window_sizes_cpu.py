@@ -21,3 +21,9 @@ def test_rows_at_d256_are_counted_in_blocks_of_four(hq, hkv, fits):
 def test_more_sequences_than_a_grid_holds():
     assert f(65535, 1, 8, 2, 128, 1000, 100, 4) > 0
     assert f(65536, 1, 8, 2, 128, 1000, 100, 4) == 0
+
+
+@pytest.mark.parametrize("n_q", [1, 3, 40])
+def test_more_than_16_query_heads_a_kv_head(n_q):
+    assert f(1, n_q, 32, 2, 128, 1000, 100, 4) > 0
+    assert f(1, n_q, 34, 2, 128, 1000, 100, 4) == 0
