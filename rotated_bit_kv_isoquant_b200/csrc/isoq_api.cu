@@ -658,6 +658,13 @@ bool valid_gqa(int n_q_heads, int n_kv_heads) {
 }
 constexpr int kMaxSeqs = 65535;  // their grid.z, and the combine's grid.y
 
+// Workspace of a planned call: a state per query row and chunk.  Chunks that meet in a cluster
+// write none; they ask for one a row, as a single chunk does.
+size_t partials_bytes(const SplitPlan& plan, int n_seqs, int n_q, int n_q_heads, int d) {
+  return (size_t)n_seqs * n_q * n_q_heads * (plan.in_cluster ? 1 : plan.n_splits) *
+         isoq::partial_stride(d) * sizeof(float);
+}
+
 // Shared by the decode entry points: validation, the split plan, then the split kernel and
 // the combine into either the output rows (out) or merged states (state).
 // window > 0: sliding-window attention with n_sinks sinks, out of type out_dtype.
@@ -680,8 +687,7 @@ int decode_common_impl(const isoq_params* params, const isoq_cache* cache, const
       window > 0 ? plan_window(n_seqs, n_q_heads, cache->n_kv_heads, cache->d, max_seq_len, n_q,
                                window, n_sinks)
                  : plan_splits(n_seqs, n_q_heads, cache->n_kv_heads, cache->d, max_seq_len, n_q);
-  const size_t need = (size_t)n_seqs * n_q * n_q_heads * plan.n_splits *
-                      isoq::partial_stride(cache->d) * sizeof(float);
+  const size_t need = partials_bytes(plan, n_seqs, n_q, n_q_heads, cache->d);
   if (workspace_bytes < need) return ISOQ_E_WORKSPACE;
   if ((rc = check_device(params))) return rc;
   isoq::DecodeArgs a{};
@@ -788,9 +794,8 @@ size_t isoq_window_workspace_bytes(int n_seqs, int n_q, int n_q_heads, int n_kv_
     return 0;
   if (!supported_d(d) || !valid_gqa(n_q_heads, n_kv_heads) || !rows_fit(n_q, n_q_heads, n_kv_heads, d))
     return 0;
-  const int ns = plan_window(n_seqs, n_q_heads, n_kv_heads, d, max_seq_len, n_q, window, n_sinks)
-                     .n_splits;
-  return (size_t)n_seqs * n_q * n_q_heads * ns * isoq::partial_stride(d) * sizeof(float);
+  return partials_bytes(plan_window(n_seqs, n_q_heads, n_kv_heads, d, max_seq_len, n_q, window, n_sinks),
+                        n_seqs, n_q, n_q_heads, d);
 }
 
 int isoq_decode_attention_window(const isoq_params* params, const isoq_cache* cache,

@@ -64,3 +64,23 @@ def test_more_sequences_than_a_grid_holds_are_refused():
         call()
         assert bool((out[:-1] != 3.0).any(-1).all()) and bool((out[-1] == 3.0).all())
     assert iq.isoq_get_status(cache) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(lens=[32768], hq=32, hkv=4, W=1024, S=4),
+                                dict(lens=[9000, 8000], hq=64, hkv=8, W=4096, S=4),
+                                dict(lens=[4000, 50], hq=16, hkv=8, W=2000, S=5, d=256),
+                                dict(lens=[3000, 0, 777], hq=15, hkv=3, W=777, S=3, bits=4),
+                                dict(lens=[40000], hq=4, hkv=1, W=38000, S=4),
+                                dict(lens=[900], hq=8, hkv=2, W=300, S=4, n_q=3),
+                                dict(lens=[900], hq=8, hkv=2, W=300, S=4, n_q=40),
+                                dict(lens=[20000], hq=8, hkv=2, W=16000, S=4, n_q=10)])
+def test_a_workspace_of_the_size_asked_for_is_enough(oracle, kw):
+    """The bytes behind it stay as they were; one byte less is refused."""
+    c = Case(seed=70, **kw)
+    n = iq.isoq_window_workspace_bytes(len(c.lens), c.n_q, c.hq, c.hkv, c.d, c.max_len, c.W, c.S)
+    raw = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    c.check(oracle, c.run(ws=raw[:n]))
+    assert bool((raw[n:] == 0xA5).all())
+    with pytest.raises(iq.IsoqError) as e:
+        c.run(ws=raw[:n - 1])
+    assert e.value.code == iq.ISOQ_E_WORKSPACE

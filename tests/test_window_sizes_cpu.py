@@ -27,3 +27,11 @@ def test_more_sequences_than_a_grid_holds():
 def test_more_than_16_query_heads_a_kv_head(n_q):
     assert f(1, n_q, 32, 2, 128, 1000, 100, 4) > 0
     assert f(1, n_q, 34, 2, 128, 1000, 100, 4) == 0
+
+
+@pytest.mark.parametrize("n_seqs,hq,hkv,d,W", [(1, 32, 4, 128, 1024), (8, 64, 8, 128, 4096), (32, 16, 8, 256, 900),
+                                               (64, 32, 8, 128, 8192)])
+def test_a_decode_that_merges_in_a_cluster_asks_for_no_partial_rows(n_seqs, hq, hkv, d, W):
+    """One row of state per query row is asked for, as of a call with a single chunk; the chunks
+    of these windows meet in shared memory."""
+    assert f(n_seqs, 1, hq, hkv, d, 32768, W, 4) == n_seqs * hq * (d + 4) * 4
