@@ -425,15 +425,20 @@ def isoq_multi_token_attention(params: Params, cache: PagedCache, Q, seq_lens, m
 
 def isoq_window_workspace_bytes(n_seqs, n_q, n_q_heads, n_kv_heads, d, max_seq_len, window,
                                 n_sinks) -> int:
-    return int(_lib.isoq_window_workspace_bytes(n_seqs, n_q, n_q_heads, n_kv_heads, d, max_seq_len,
-                                                window, n_sinks))
+    """0 for sizes that the windowed calls refuse."""
+    sizes = (n_seqs, n_q, n_q_heads, n_kv_heads, d, max_seq_len, window, n_sinks)
+    if not all(0 <= x < 2 ** 31 for x in sizes):  # would wrap on the way into a C int
+        return 0
+    return int(_lib.isoq_window_workspace_bytes(*sizes))
 
 
-def _check_window(cache, Q, seq_lens, out, workspace, window, n_sinks):
+def _check_window(cache, Q, seq_lens, max_seq_len, out, workspace, window, n_sinks):
     """The tensors of a windowed call agree in shape and live on the cache's device, and the
     numbers fit the C interface's ints."""
     if not (0 < window < 2 ** 31 and 0 <= n_sinks < 2 ** 31):
         raise ValueError("window must be in [1, 2^31), n_sinks in [0, 2^31)")
+    if not 0 <= max_seq_len < 2 ** 31:
+        raise ValueError("max_seq_len must be in [0, 2^31)")
     if Q.shape != out.shape or Q.shape[-1] != cache.d:
         raise ValueError(f"Q and out must have the same shape ending in d = {cache.d}")
     if seq_lens.numel() < Q.shape[0]:
@@ -453,7 +458,7 @@ def isoq_decode_attention_window(params: Params, cache: PagedCache, Q, seq_lens,
     import torch
     if Q.dim() != 3:
         raise ValueError("Q must be [n_seqs][n_q_heads][d]")
-    _check_window(cache, Q, seq_lens, out, workspace, window, n_sinks)
+    _check_window(cache, Q, seq_lens, max_seq_len, out, workspace, window, n_sinks)
     _check(_lib.isoq_decode_attention_window(
         params.handle, cache._c, _dev_ptr(Q, "Q"), _dtype_code(Q), Q.shape[0], Q.shape[1],
         _dev_ptr(seq_lens, "seq_lens", torch.int32), max_seq_len, window, n_sinks,
@@ -472,7 +477,7 @@ def isoq_multi_token_attention_window(params: Params, cache: PagedCache, Q, seq_
     import torch
     if Q.dim() != 4:
         raise ValueError("Q must be [n_seqs][n_q][n_q_heads][d]")
-    _check_window(cache, Q, seq_lens, out, workspace, window, n_sinks)
+    _check_window(cache, Q, seq_lens, max_seq_len, out, workspace, window, n_sinks)
     _check(_lib.isoq_multi_token_attention_window(
         params.handle, cache._c, _dev_ptr(Q, "Q"), _dtype_code(Q), Q.shape[0], Q.shape[1],
         Q.shape[2], _dev_ptr(seq_lens, "seq_lens", torch.int32), max_seq_len, window, n_sinks,

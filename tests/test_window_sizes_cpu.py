@@ -35,3 +35,17 @@ def test_a_decode_that_merges_in_a_cluster_asks_for_no_partial_rows(n_seqs, hq, 
     """One row of state per query row is asked for, as of a call with a single chunk; the chunks
     of these windows meet in shared memory."""
     assert f(n_seqs, 1, hq, hkv, d, 32768, W, 4) == n_seqs * hq * (d + 4) * 4
+
+
+def test_numbers_beyond_an_int_are_not_wrapped():
+    good = [1, 1, 8, 2, 128, 1000, 100, 4]
+    assert iq.isoq_window_workspace_bytes(*good) > 0
+    for i in range(len(good)):
+        for n in (2 ** 31, 2 ** 32 + good[i], -2 ** 32 + good[i]):
+            assert iq.isoq_window_workspace_bytes(*good[:i], n, *good[i + 1:]) == 0, (i, n)
+    Q, lens, ws = torch.zeros(2, 8, 128), torch.zeros(2, dtype=torch.int32), torch.zeros(16)
+    for n in (2 ** 31, 2 ** 32 + 16, -1):
+        with pytest.raises(ValueError, match="max_seq_len"):
+            iq.isoq_decode_attention_window(None, _Cache, Q, lens, n, 16, 4, Q, 1.0, ws)
+        with pytest.raises(ValueError, match="max_seq_len"):
+            iq.isoq_multi_token_attention_window(None, _Cache, Q[:, None], lens, n, 16, 4, Q[:, None], 1.0, ws)
