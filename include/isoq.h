@@ -420,6 +420,9 @@ int isoq_multi_token_attention(const isoq_params* params, const isoq_cache* cach
  * codes, any norms, infinities and NaN included): a caller may recycle a page for another
  * sequence as soon as the window has passed its last token.
  *
+ * Q's elements may be of any size up to 2^100 with a scale to match: a query is scaled by a power
+ * of two of its own where binary16 operands would not hold it.
+ *
  * window >= 1, n_sinks >= 0.  max_seq_len: a host upper bound of seq_lens, the one given
  * to isoq_window_workspace_bytes; a longer seq_lens[s] is clamped to it (and to the page
  * table) with ISOQ_ST_LEN_RANGE, a negative one is 0.  Q, out: device, 16-byte aligned;

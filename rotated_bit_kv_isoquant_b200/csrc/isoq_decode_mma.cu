@@ -51,7 +51,8 @@ struct MmaSmem {
   static constexpr int kBarOff = kRing;
   static constexpr int kAOff = kBarOff + NW * NST * 8;
   static constexpr int kRowOff = kAOff + (D / 16) * 32 * 16;  // int [8]: output row per CTA row
-  static constexpr int kBytes = kRowOff + 8 * 4;
+  static constexpr int kUnitOff = kRowOff + 8 * 4;            // float [8]: query_exponent's 2^e
+  static constexpr int kBytes = kUnitOff + 8 * 4;
   // the warps' states [NW][8][D + 4] and the merged rows [8][D + 4]
   static constexpr int kMergeBytes = NW * 8 * (D + 4) * 4 + 8 * (D + 4) * 4;
   static_assert(kMergeBytes <= kRing, "merge buffer must fit in the ring");
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
   uint4* qa = reinterpret_cast<uint4*>(smem + SM::kAOff);
   int* row_off = reinterpret_cast<int*>(smem + SM::kRowOff);
+  float* unit = reinterpret_cast<float*>(smem + SM::kUnitOff);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -207,6 +209,12 @@ __global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
       float z[E];
 #pragma unroll
       for (int k = 0; k < NB; ++k) mat_fwd(pq[k], v + 4 * k, z + 4 * k);
+      const int ex = query_exponent<E>(z);
+      if (ex != 0) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) z[i] *= pow2i(-ex);
+      }
+      if (lane == 0) unit[h] = pow2i(ex);
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         const int base = lane * E + 4 * k;  // dims base..base+3
@@ -240,7 +248,8 @@ __global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
   float acc[KS][4];
 #pragma unroll
   for (int i = 0; i < KS; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  const float kf = scale * kLog2e / (ALPHA * (float)D);  // log2 score per (dot * nK)
+  // log2 score of row g per (dot * nK)
+  const float kf = scale * kLog2e / (ALPHA * (float)D) * unit[g];
 
   bool timed_out = false;
   int k = 0;

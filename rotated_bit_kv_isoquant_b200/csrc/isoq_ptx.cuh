@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <math_constants.h>
 #include <stdint.h>
 
 #include "isoq_common.cuh"
@@ -63,6 +64,23 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// A rotated query row z (the warp holds it, E elements a lane) is split into a binary16 high and
+// low part, which keep 2^-22 of the row's largest element while that lies in [kQueryMin, kQueryMax):
+// below, the low parts run into the subnormals, above, the high parts into infinity.  Other rows
+// are divided by 2^e first, which brings their largest into [1, 2), and their scores multiplied by
+// it; e = 0 leaves a row's bits as they are.  Queries up to 2^100 in size.
+constexpr float kQueryMin = 0.125f, kQueryMax = 32768.f;
+template <int E>
+__device__ __forceinline__ int query_exponent(const float (&z)[E]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) m = max(m, __float_as_uint(z[i]) & 0x7FFFFFFFu);
+  const float top = __uint_as_float(__reduce_max_sync(kFull, m));  // magnitudes order as their bits do
+  if ((top >= kQueryMin && top < kQueryMax) || top == 0.f || !(top < CUDART_INF_F)) return 0;
+  return max(-100, min(100, (int)(__float_as_uint(top) >> 23) - 127));
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {

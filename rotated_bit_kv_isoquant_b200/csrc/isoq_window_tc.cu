@@ -75,7 +75,8 @@ struct WinSmem {
   static constexpr int kOffRed = kOffMeta + 32;         // float [2]
   static constexpr int kOffMl = kOffRed + 16;           // float2 [2 halves][128]: m, l
   static constexpr int kOffRow = kOffMl + 256 * 8;      // int [256]: output row of each row
-  static constexpr int kOffBar = kOffRow + 256 * 4;
+  static constexpr int kOffUnit = kOffRow + 256 * 4;    // float [256]: query_exponent's 2^e by softmax thread
+  static constexpr int kOffBar = kOffUnit + 256 * 4;
   static constexpr int kOffTmem = kOffBar + kBars * 8 + 8;
   static constexpr int kBytes = kOffTmem + 16;
   static_assert(kOffRing % 16 == 0 && kBB % 16 == 0 && kOffBar % 8 == 0 && kOffNorm % 16 == 0, "");
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   float* red = reinterpret_cast<float*>(smem + SM::kOffRed);
   float2* ml = reinterpret_cast<float2*>(smem + SM::kOffMl);
   int* row_off = reinterpret_cast<int*>(smem + SM::kOffRow);
+  float* unit = reinterpret_cast<float*>(smem + SM::kOffUnit);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kOffTmem);
   const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + SM::kOffK), sV = smem_u32(smem + SM::kOffV);
 
@@ -177,7 +179,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (n > 1) issue(1, entry_of(1));
   }
 
-  if (tid < 256) row_off[tid] = tid < nh ? row_index(tid) : n_q * n_q_heads;
+  if (tid < 256) {
+    row_off[tid] = tid < nh ? row_index(tid) : n_q * n_q_heads;
+    unit[tid] = 1.f;
+  }
   float sgn[5];  // the lane's side of each cross-lane stage of the WHT
 #pragma unroll
   for (int i = 0; i < 5; ++i) sgn[i] = ((lane >> i) & 1) ? -1.f : 1.f;
@@ -210,11 +215,37 @@ __global__ void __launch_bounds__(kWThreads, 1)
       load(r0 + kWWarps * kAt, nx);
 #pragma unroll
       for (int j = 0; j < kAt; ++j) wht_signed<E>(v[j], sgn);
+      // z, and whether a row's largest element lies outside the range that needs no division
+      uint32_t sizes = 0;  // bit j: row j has an element >= 2^-3 (or is none), bit 4 + j: >= 2^15
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        float z[E];
+        mat_fwd(M, v[j], z);
+        float big = r0 + kWWarps * j < nh ? 0.f : 1.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          v[j][e] = z[e];
+          big = fmaxf(big, fabsf(z[e]));
+        }
+        sizes |= (big >= kQueryMin ? 1u << j : 0u) | (big >= kQueryMax ? 16u << j : 0u);
+      }
+      if (__reduce_or_sync(kFull, sizes) != 15u) {  // out of line: code that does not run is not fetched
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) {
+          const int r = r0 + kWWarps * j, ex = query_exponent<E>(v[j]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[j][e] *= pow2i(-ex);
+          if (lane == 0 && in_bounds(r < rows_cta, status)) {
+            unit[r] = pow2i(ex);
+            if (!two) unit[128 + r] = pow2i(ex);  // both halves hold the row
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < kAt; ++j) {
         const int r = r0 + kWWarps * j;
-        float z[E], hi[E];
-        mat_fwd(M, v[j], z);
+        const float (&z)[E] = v[j];
+        float hi[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) hi[e] = __half2float(__float2half_rn(z[e]));
         const uint32_t at = sQ + (r >> 7) * 2 * SM::kQPart + (k0 >> 3) * SM::kQGroup +
@@ -412,6 +443,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int my_lo = win_lo<true>(win, my_lim);
     const uint32_t t_s = t_lane + col_s(w), t_p = t_lane + col_p(w), t_o = t_lane + col_o(w);
     const int n_jobs = jobs(w);
+    // a warp with a divided row (query_exponent) has no page that goes unmasked: the common path is
+    // without its multiplication (as a branch of every page it cost 1.6% of a long chunk)
+    const int full_to = __any_sync(kFull, unit[tid] != 1.f) ? -1 : lim_lo;
     for (int i = 0; i < n_jobs; ++i) {
       const int k = two ? i : 2 * i + w, st = k & st_mask;
       // the page's scores (warp-uniform: collective loads follow), then its norms
@@ -435,13 +469,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const float sg = sig[st];
       const float vr = sg > sigma ? sigma / sg : 1.f;  // 0 on the first valid page
       sigma = sg;
-      const bool all = page_ok && tok0 + kPage <= lim_lo && wp.page_full(win, tok0);
+      const bool all = page_ok && tok0 + kPage <= full_to && wp.page_full(win, tok0);
       // exponents a_j = s_j |k_j| - m2 from one FMA each; m2 moves only when some a_j > kLazy (or
       // on the row's first scores), and then O is rescaled in place, factor resc
       float resc = vr;
       bool moved = vr != 1.f;
       auto exponents = [&](auto full_c) {
         constexpr bool FULL = decltype(full_c)::value;
+        if (!FULL && __any_sync(kFull, unit[threadIdx.x] != 1.f)) {
+          const float mul = unit[threadIdx.x];
+#pragma unroll
+          for (int j = 0; j < 64; ++j) x[j] *= mul;
+        }
         auto sees = [&](int tok) { return page_ok && tok < my_lim && win_sees<true>(win, my_lo, tok); };
         const bool fresh = m2 == -CUDART_INF_F;
         const float2 nm2 = fresh ? make_float2(0.f, 0.f) : make_float2(-m2, -m2);
