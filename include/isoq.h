@@ -322,7 +322,9 @@ int isoq_dequantize_rope(const isoq_params* params, const isoq_cache* cache,
  * scale at which they round by < 2e-5, the weights p |v| / sigma) with binary32
  * accumulation.  Measured against a binary64 evaluation of the same codes: relative L2
  * error per (sequence, head) <= 5e-4 on the five test workloads.  2 and 4 bits: binary16
- * operands throughout, the query as a high and a low binary16 part.
+ * operands throughout, the query as a high and a low binary16 part, so that |Q| sqrt(d) of a
+ * query has to stay below 65504 (in every format for chunks of at least 16 rows, (query token,
+ * query head) pairs, per KV head at d = 128; the windowed calls take any size).
  *
  * Q: device [n_seqs][n_q_heads][d], element type q_dtype.  seq_lens: device int32
  * [n_seqs], the number of cached tokens each query attends (0 gives an all-zero output;

@@ -209,12 +209,13 @@ __global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
       float z[E];
 #pragma unroll
       for (int k = 0; k < NB; ++k) mat_fwd(pq[k], v + 4 * k, z + 4 * k);
-      const int ex = query_exponent<E>(z);
+      // the whole-context decode takes its queries as they are: a factor per row costs it 1-2%
+      const int ex = WIN ? query_exponent<E>(z) : 0;
       if (ex != 0) {
 #pragma unroll
         for (int i = 0; i < E; ++i) z[i] *= pow2i(-ex);
       }
-      if (lane == 0) unit[h] = pow2i(ex);
+      if (WIN && lane == 0) unit[h] = pow2i(ex);
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         const int base = lane * E + 4 * k;  // dims base..base+3
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
 #pragma unroll
   for (int i = 0; i < KS; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   // log2 score of row g per (dot * nK)
-  const float kf = scale * kLog2e / (ALPHA * (float)D) * unit[g];
+  const float kf = scale * kLog2e / (ALPHA * (float)D) * (WIN ? unit[g] : 1.f);
 
   bool timed_out = false;
   int k = 0;
