@@ -430,7 +430,10 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
   // from lanes 8t and 8t + 4.
   float m2 = -CUDART_INF_F;  // running max of the log2 scores of row rg
   float lsum = 0.f;          // this lane's share of sum p of row rg
-  float sigma = 0.f;         // V-norm reference (warp-uniform)
+  // V-norm reference: warp-uniform; in chunks of a window, whose rows see different tokens, the
+  // row's own, so that a large |v| which it does not see costs its weights no bits
+  constexpr bool ROW_SIGMA = WIN && MQ;
+  float sigma = 0.f;
   float inv_sigma = 0.f;
   float acc[MT][4];
 #pragma unroll
@@ -549,9 +552,14 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
           for (int c = 0; c < 2; ++c) {
             const int tok = tok0 + tk + c;
             const bool vld = page_ok && tok < lim_hi && wp.any_sees(win, tok);
-            sv[n][c] = vld && (!MQ || (tok < lim_g && win_sees<WIN>(win, lo_g, tok)))
-                           ? sv[n][c] : -CUDART_INF_F;
-            nv[n][c] = vld ? nv[n][c] : 0.f;
+            if constexpr (ROW_SIGMA) {
+              const bool mine = vld && tok < lim_g && win_sees<WIN>(win, lo_g, tok);
+              sv[n][c] = mine ? sv[n][c] : -CUDART_INF_F;
+              nv[n][c] = mine ? nv[n][c] : 0.f;
+            } else {
+              sv[n][c] = vld && (!MQ || tok < lim_g) ? sv[n][c] : -CUDART_INF_F;
+              nv[n][c] = vld ? nv[n][c] : 0.f;
+            }
           }
         }
       }
@@ -577,12 +585,13 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
           m2 = tmax;
         }
         float vr = 1.f;
-        if (vmax > vthr) {   // warp-uniform
+        if (vmax > vthr) {   // warp-uniform unless ROW_SIGMA
           vr = sigma / vmax;  // 0 on the first valid tile
           sigma = vmax;
           inv_sigma = 1.f / vmax;
         }
         // columns 2t, 2t+1 are rows 2t, 2t+1 (RB = 4: rows 2t & 3, unused for t >= 2)
+        if constexpr (ROW_SIGMA) resc *= vr, vr = 1.f;
         const float r0 = __shfl_sync(kFull, resc, 4 * ((2 * t) % RB)) * vr;
         const float r1 = __shfl_sync(kFull, resc, 4 * ((2 * t + 1) % RB)) * vr;
 #pragma unroll
@@ -693,6 +702,8 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
     // m-tile mt = 8 up + 4 p + b, rows g / g + 8 = dims 8u + 2b / + 1 with u = 2 (g + 8 up)
     // + p (b = 3: the spare unit, dims 8u + 6, 8u + 7); columns 2t, 2t+1 = rows
     const float f = sigma / ALPHA;
+    const float f0 = ROW_SIGMA ? __shfl_sync(kFull, f, 4 * ((2 * t) % RB)) : f;
+    const float f1 = ROW_SIGMA ? __shfl_sync(kFull, f, 4 * ((2 * t + 1) % RB)) : f;
     if (2 * t < RB) {
 #pragma unroll
       for (int up = 0; up < NU; ++up)
@@ -705,10 +716,10 @@ __global__ void __launch_bounds__(NW * 32, i8_min_blocks<D>(NW))
             if (!in_bounds(d0 + 1 < D && 2 * t + 1 < 8, status)) continue;
             float* r0 = mb + (warp * 8 + 2 * t) * PS;
             float* r1 = mb + (warp * 8 + 2 * t + 1) * PS;
-            r0[d0] = acc[mt][0] * f;
-            r1[d0] = acc[mt][1] * f;
-            r0[d0 + 1] = acc[mt][2] * f;
-            r1[d0 + 1] = acc[mt][3] * f;
+            r0[d0] = acc[mt][0] * f0;
+            r1[d0] = acc[mt][1] * f1;
+            r0[d0 + 1] = acc[mt][2] * f0;
+            r1[d0 + 1] = acc[mt][3] * f1;
           }
     }
     if (t == 0 && g < RB) {

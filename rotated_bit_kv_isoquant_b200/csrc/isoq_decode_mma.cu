@@ -244,7 +244,10 @@ __global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
   // this lane are heads 2t, 2t+1, whose rescale factors come from lanes 8t and 8t + 4.
   float m2 = -CUDART_INF_F;  // running max of the log2 scores of head g
   float lsum = 0.f;          // this lane's share of sum p of head g
-  float sigma = 0.f;         // V-norm reference (warp-uniform)
+  // V-norm reference: warp-uniform; in chunks of a window, whose rows see different tokens, the
+  // row's own, so that a large |v| which it does not see costs its weights no bits
+  constexpr bool ROW_SIGMA = WIN && MQ;
+  float sigma = 0.f;
   float inv_sigma = 0.f;
   float acc[KS][4];
 #pragma unroll
@@ -322,12 +325,19 @@ __global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
           const int tok = tok0 + tk;
           const bool v0 = page_ok && tok < lim_hi && wp.any_sees(win, tok);
           const bool v1 = page_ok && tok + 1 < lim_hi && wp.any_sees(win, tok + 1);
-          sv[n][0] = v0 && (!MQ || (tok < lim_g && win_sees<WIN>(win, lo_g, tok)))
-                         ? sv[n][0] : -CUDART_INF_F;
-          sv[n][1] = v1 && (!MQ || (tok + 1 < lim_g && win_sees<WIN>(win, lo_g, tok + 1)))
-                         ? sv[n][1] : -CUDART_INF_F;
-          nv[n][0] = v0 ? nv[n][0] : 0.f;
-          nv[n][1] = v1 ? nv[n][1] : 0.f;
+          if constexpr (ROW_SIGMA) {
+            const bool m0 = v0 && tok < lim_g && win_sees<WIN>(win, lo_g, tok);
+            const bool m1 = v1 && tok + 1 < lim_g && win_sees<WIN>(win, lo_g, tok + 1);
+            sv[n][0] = m0 ? sv[n][0] : -CUDART_INF_F;
+            sv[n][1] = m1 ? sv[n][1] : -CUDART_INF_F;
+            nv[n][0] = m0 ? nv[n][0] : 0.f;
+            nv[n][1] = m1 ? nv[n][1] : 0.f;
+          } else {
+            sv[n][0] = v0 && (!MQ || tok < lim_g) ? sv[n][0] : -CUDART_INF_F;
+            sv[n][1] = v1 && (!MQ || tok + 1 < lim_g) ? sv[n][1] : -CUDART_INF_F;
+            nv[n][0] = v0 ? nv[n][0] : 0.f;
+            nv[n][1] = v1 ? nv[n][1] : 0.f;
+          }
         }
       }
       // this lane's largest score and V norm of the tile (three-input max instructions)
@@ -352,11 +362,12 @@ __global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
           m2 = tmax;
         }
         float vr = 1.f;
-        if (vmax > vthr) {   // warp-uniform
+        if (vmax > vthr) {   // warp-uniform unless ROW_SIGMA
           vr = sigma / vmax;  // 0 on the first valid tile
           sigma = vmax;
           inv_sigma = 1.f / vmax;
         }
+        if constexpr (ROW_SIGMA) resc *= vr, vr = 1.f;
         const float r0 = __shfl_sync(kFull, resc, 8 * t) * vr;
         const float r1 = __shfl_sync(kFull, resc, 8 * t + 4) * vr;
 #pragma unroll
@@ -466,6 +477,8 @@ __global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
   {
     // acc_true = acc * sigma / ALPHA (times 1 / exp2(m2) in the log2 frame)
     const float f = sigma / ALPHA;
+    const float f0 = ROW_SIGMA ? __shfl_sync(kFull, f, 8 * t) : f;
+    const float f1 = ROW_SIGMA ? __shfl_sync(kFull, f, 8 * t + 4) : f;
 #pragma unroll
     for (int gq = 0; gq < NG; ++gq) {
 #pragma unroll
@@ -476,10 +489,10 @@ __global__ void __launch_bounds__(NW * 32, dec_min_blocks<D>(NW))
         if (!in_bounds(d0 + 1 < D && 2 * t + 1 < 8, status)) continue;
         float* r0 = mb + (warp * 8 + 2 * t) * PS;
         float* r1 = mb + (warp * 8 + 2 * t + 1) * PS;
-        r0[d0] = acc[8 * gq + mt][0] * f;
-        r1[d0] = acc[8 * gq + mt][1] * f;
-        r0[d0 + 1] = acc[8 * gq + mt][2] * f;
-        r1[d0 + 1] = acc[8 * gq + mt][3] * f;
+        r0[d0] = acc[8 * gq + mt][0] * f0;
+        r1[d0] = acc[8 * gq + mt][1] * f1;
+        r0[d0 + 1] = acc[8 * gq + mt][2] * f0;
+        r1[d0 + 1] = acc[8 * gq + mt][3] * f1;
       }
     }
     if (t == 0) {

@@ -11,7 +11,9 @@
 //   warp 12      one thread issues the products: scores S = Q~hi K_hat^T + Q~lo K_hat^T and
 //                O += P' V_hat, accumulators in tensor memory
 //   warps 0-3,   softmax: thread r owns row r of its half (tensor-memory lane r), reads its 64
-//   warps 4-7    scores, keeps its running maximum and sum, writes P' = p |v| / sigma
+//   warps 4-7    scores, keeps its running maximum and sum, writes P' = p |v| / sigma, sigma the
+//                largest |v| that a row of the CTA sees; lift_bits says what is done for a row that
+//                sees much smaller ones
 // With more than 128 rows per KV head the two softmax halves hold two blocks of 128 rows and
 // share every page's tiles (256 rows for one dequantisation); with fewer both hold the same
 // rows and take the pages in turn, and their states are merged at the end.  So one half's
@@ -56,6 +58,9 @@ __device__ __forceinline__ constexpr uint32_t col_s(int w) { return 64 * w; }
 __device__ __forceinline__ constexpr uint32_t col_p(int w) { return 128 + 32 * w; }
 __device__ __forceinline__ constexpr uint32_t col_o(int w) { return 256 + 128 * w; }
 
+// A page as the softmax takes it: it has data; some row may need a lift on it (lift_bits: a token
+// that some row sees has |v| < sigma / kSpreadNorms); none does, but on the half's page before.
+enum PageState { kValid = 1, kSpread = 2, kLevel = 4 };
 enum Bar {  // mbarriers: of the ring (2), the tile stages (up to 4), the softmax halves (2)
   kRing = 0, kKFull = 2, kVFull = 6, kKFree = 10, kVFree = 14,
   kSFull = 18, kSRead = 20, kPFull = 22, kPvDone = 24, kDrain = 26, kBars = 27
@@ -71,8 +76,9 @@ struct WinSmem {
   static constexpr int kOffV = kOffK + 2 * kPageTile;   // [2] V_hat tiles
   static constexpr int kOffRing = kOffV + 2 * kPageTile;
   static constexpr int kOffNorm = kOffRing + 2 * kBB;   // float [4 stages][64 K | 64 V]
-  static constexpr int kOffMeta = kOffNorm + 4 * 128 * 4;  // float [4] sigma, int [4] page is valid
-  static constexpr int kOffRed = kOffMeta + 32;         // float [2]
+  static constexpr int kOffMeta = kOffNorm + 4 * 128 * 4;  // float [4] sigma, int [4] PageState,
+                                                        // float [4] largest |v| that a row sees
+  static constexpr int kOffRed = kOffMeta + 48;         // float2 [2]
   static constexpr int kOffMl = kOffRed + 16;           // float2 [2 halves][128]: m, l
   static constexpr int kOffRow = kOffMl + 256 * 8;      // int [256]: output row of each row
   static constexpr int kOffUnit = kOffRow + 256 * 4;    // float [256]: query_exponent's 2^e by softmax thread
@@ -103,7 +109,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
   float* nrm = reinterpret_cast<float*>(smem + SM::kOffNorm);
   float* sig = reinterpret_cast<float*>(smem + SM::kOffMeta);
   int* valid = reinterpret_cast<int*>(smem + SM::kOffMeta) + 4;
-  float* red = reinterpret_cast<float*>(smem + SM::kOffRed);
+  float* top = reinterpret_cast<float*>(smem + SM::kOffMeta) + 8;
+  float2* red = reinterpret_cast<float2*>(smem + SM::kOffRed);
   float2* ml = reinterpret_cast<float2*>(smem + SM::kOffMl);
   int* row_off = reinterpret_cast<int*>(smem + SM::kOffRow);
   float* unit = reinterpret_cast<float*>(smem + SM::kOffUnit);
@@ -294,6 +301,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     uint32_t tl0, tl1, th0, th1;
     level_tables<BITS>(tl0, tl1, th0, th1);
     const float kf = scale * kLog2e / (ALPHA * (float)D);  // log2 score per (dot * nK)
+    int spreads = 0;  // bit 0: the page before of the same softmax half was spread
     int issued = min(n, 2), k = 0;
     // page-table entries of pages k .. k + 2, each loaded three pages ahead of its use
     int ph0 = entry_of(0), ph1 = entry_of(1), ph2 = entry_of(2);
@@ -326,17 +334,24 @@ __global__ void __launch_bounds__(kWThreads, 1)
         } else {
           const int j = t - 64;
           float nv = half_at(blk + v_norm_off(D, BITS) + 2 * j);
-          nv = page_ok && tok0 + j < lim_hi && wp.any_sees(win, tok0 + j) ? nv : 0.f;
-          float pm = warp_max(nv);
-          if (lane == 0) red[warp - 10] = pm;
+          const bool seen = page_ok && tok0 + j < lim_hi && wp.any_sees(win, tok0 + j);
+          nv = seen ? nv : 0.f;
+          // largest and smallest (norms, >= 0, order as their bits do)
+          const uint32_t pm2 = __reduce_max_sync(kFull, __float_as_uint(nv));
+          const uint32_t pl2 = __reduce_min_sync(kFull, __float_as_uint(seen ? nv : CUDART_INF_F));
+          if (lane == 0) red[warp - 10] = make_float2(__uint_as_float(pm2), __uint_as_float(pl2));
           asm volatile("bar.sync 1, 64;" ::: "memory");  // warps 10 and 11
-          pm = fmaxf(red[0], red[1]);
+          const float4 both = *reinterpret_cast<const float4*>(red);
+          const float pm = fmaxf(both.x, both.z), pl = fminf(both.y, both.w);
           sigma = pm > sigma * kSigmaSlack ? pm : sigma;
+          const bool spread = sigma > kSpreadNorms * pl, before_spread = spreads & 1;
+          spreads = two ? spread : spreads >> 1 | (spread ? 2 : 0);
           if (ok) {
             nrm[st * 128 + t] = sigma > 0.f ? nv * (1.f / sigma) : 0.f;
             if (t == 64) {
               sig[st] = sigma;
-              valid[st] = page_ok;
+              top[st] = pm;
+              valid[st] = (page_ok ? kValid : 0) | (spread ? kSpread : before_spread ? kLevel : 0);
             }
           }
         }
@@ -446,6 +461,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     // a warp with a divided row (query_exponent) has no page that goes unmasked: the common path is
     // without its multiplication (as a branch of every page it cost 1.6% of a long chunk)
     const int full_to = __any_sync(kFull, unit[tid] != 1.f) ? -1 : lim_lo;
+    float lim = kLazy + kLift;  // of an exponent: kLazy plus the row's lift
     for (int i = 0; i < n_jobs; ++i) {
       const int k = two ? i : 2 * i + w, st = k & st_mask;
       // the page's scores (warp-uniform: collective loads follow), then its norms
@@ -464,16 +480,40 @@ __global__ void __launch_bounds__(kWThreads, 1)
       ok = __all_sync(kFull, mbar_wait(bars + kVFull + st, (k >> st_log) & 1));
       if (!ok) break;
       const float* nk = nrm + st * 128;
-      const bool page_ok = valid[st] != 0;
+      const int state = valid[st];
+      const bool page_ok = (state & kValid) != 0;
       const int tok0 = wp.page(p_begin + k) * kPage;
       const float sg = sig[st];
       const float vr = sg > sigma ? sigma / sg : 1.f;  // 0 on the first valid page
       sigma = sg;
-      const bool all = page_ok && tok0 + kPage <= full_to && wp.page_full(win, tok0);
-      // exponents a_j = s_j |k_j| - m2 from one FMA each; m2 moves only when some a_j > kLazy (or
-      // on the row's first scores), and then O is rescaled in place, factor resc
+      // exponents a_j = s_j |k_j| - m2 from one FMA each; m2, the row's running maximum less its lift,
+      // moves only when some a_j > lim, kLazy above that maximum (or on the row's first scores), and
+      // then O is rescaled in place, factor resc
       float resc = vr;
       bool moved = vr != 1.f;
+      auto sees = [&](int tok) { return page_ok && tok < my_lim && win_sees<true>(win, my_lo, tok); };
+      const bool all = page_ok && tok0 + kPage <= full_to && wp.page_full(win, tok0);
+      if (state & (kSpread | kLevel)) {  // the row's lift
+        float bits = 0.f;
+        if (state & kSpread) {
+          float v = top[st];
+          if (!all) {
+            v = 0.f;
+#pragma unroll 4
+            for (int j = 0; j < 64; ++j) v = fmaxf(v, sees(tok0 + j) ? nk[64 + j] : 0.f);
+            v *= sg;
+          }
+          bits = lift_bits(v, sg, lim - (kLazy + kLift));
+        }
+        const float up = lim - (kLazy + kLift + bits);  // what m2 rises by
+        if (up != 0.f) {
+          lim -= up;
+          m2 += up;
+          lsum *= ex2(-up);
+          resc *= ex2(-up);
+          moved = true;
+        }
+      }
       auto exponents = [&](auto full_c) {
         constexpr bool FULL = decltype(full_c)::value;
         if (!FULL && __any_sync(kFull, unit[threadIdx.x] != 1.f)) {
@@ -481,7 +521,6 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
           for (int j = 0; j < 64; ++j) x[j] *= mul;
         }
-        auto sees = [&](int tok) { return page_ok && tok < my_lim && win_sees<true>(win, my_lo, tok); };
         const bool fresh = m2 == -CUDART_INF_F;
         const float2 nm2 = fresh ? make_float2(0.f, 0.f) : make_float2(-m2, -m2);
         float am[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
@@ -500,14 +539,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
           }
         }
         const float amax = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
-        if (fresh ? amax != -CUDART_INF_F : amax > kLazy) {
-          const float f = fresh ? 0.f : ex2(-amax);  // fresh: nothing accumulated yet
+        if (fresh ? amax != -CUDART_INF_F : amax > lim) {
+          const float up = amax - (lim - kLazy);
+          const float f = fresh ? 0.f : ex2(-up);  // fresh: nothing accumulated yet
           resc *= f;
           lsum *= f;
-          m2 = fresh ? amax : m2 + amax;
+          m2 = fresh ? up : m2 + up;
           moved = true;
 #pragma unroll
-          for (int j = 0; j < 64; ++j) x[j] -= amax;
+          for (int j = 0; j < 64; ++j) x[j] -= up;
         }
       };
       if (all) exponents(std::true_type{});
