@@ -71,9 +71,7 @@ extern "C" {
  * rotating the block y_b (read as the quaternion w + x i + y j + z k, Hamilton
  * convention) to z_b = p_b * y_b * conj(q_b).  That is d/4 * 8 = 256 stored parameters
  * per head at d = 128 (the paper's count, versus d^2 = 16,384 for a dense rotation).
- * (A handle also keeps derived device copies: the blocks as matrices, 4 d floats per head,
- * and for the read-back the dense inverse rotation in two binary16 parts, 4 d^2 bytes per
- * head.)
+ * (A handle also keeps a derived device copy: the blocks as matrices, 4 d floats per head.)
  * K and V of one KV head share the same parameters.
  *
  * Values are drawn from SplitMix64 (Steele, Lea & Flood, OOPSLA 2014) seeded with `seed`:

@@ -1,6 +1,5 @@
 // C-ABI layer of libisoq: argument validation, rotation parameters, launch configuration.
 // See include/isoq.h for the contract of every entry point.
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -22,7 +21,6 @@ struct isoq_params {
   float* dev;               // the parameters as generated (SO(4): [H][d/4][2][4] quaternions,
                             // the 256 parameters/head; SO(2): [H][d/2][2] cos, sin)
   float* dev_mat;           // [n_kv_heads][d/4][4][4] derived: each 4-dim block's matrix
-  __half* dev_rot;          // derived: the inverse rotation as matrix operands (rotation_parts)
   std::vector<float> host;  // same values as dev
 };
 
@@ -68,33 +66,6 @@ void hamilton(const double* a, const double* b, double* o) {
   o[1] = a[0] * b[1] + a[1] * b[0] + a[2] * b[3] - a[3] * b[2];
   o[2] = a[0] * b[2] - a[1] * b[3] + a[2] * b[0] + a[3] * b[1];
   o[3] = a[0] * b[3] + a[1] * b[2] - a[2] * b[1] + a[3] * b[0];
-}
-
-// The inverse rotation x = R^T z of every head as operands of the read-back's matrix product
-// (column n of its 128-wide half q is dim read_column(d, q, n); k = the rotated dim):
-// kRotScale R[k][n] split into two binary16 parts, hi + lo, each in the tensor core's
-// no-swizzle K-major layout.  [head][half q][part][k / 8][n / 8][n % 8][k % 8].  R in
-// binary64 from the 4x4 block matrices: R[k][n] = sum_j M[k][j] H[4 (k/4) + j][n] / sqrt(d).
-// One thread per entry.
-__global__ void rotation_parts_kernel(const float* __restrict__ mats, __half* __restrict__ out,
-                                      int d, int n_kv_heads) {
-  const size_t part = (size_t)d * 128, entries = (size_t)n_kv_heads * d * d;
-  const double unit = isoq::kRotScale / sqrt((double)d);
-  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < entries;
-       i += (size_t)gridDim.x * blockDim.x) {
-    const size_t hq = i / part;  // head * (d / 128) + q
-    const int k = (int)(i % part) / 128, n = (int)(i % 128);
-    const int h = (int)(hq / (d / 128)), q = (int)(hq % (d / 128));
-    const int dim = isoq::read_column(d, q, n);
-    const float* M = mats + ((size_t)h * (d / 4) + k / 4) * 16 + (k & 3) * 4;
-    double r = 0.0;
-    for (int j = 0; j < 4; ++j)  // Sylvester: H[a][b] = (-1)^popcount(a & b)
-      r += (__popc((4 * (k / 4) + j) & dim) & 1) ? -(double)M[j] : (double)M[j];
-    r *= unit;
-    __half* hi = out + hq * 2 * part + (size_t)(k / 8) * 1024 + (n / 8) * 64 + (n % 8) * 8 + k % 8;
-    hi[0] = __float2half_rn((float)r);
-    hi[part] = __float2half_rn((float)(r - (double)__half2float(hi[0])));
-  }
 }
 
 // SM count of the current device (148 on B200 when no device can be queried, which keeps
@@ -353,7 +324,6 @@ int isoq_make_params_v(uint64_t seed, int d, int n_kv_heads, int bits, int rotat
   p->rotation = rotation;
   p->dev = nullptr;
   p->dev_mat = nullptr;
-  p->dev_rot = nullptr;
   p->host.resize((size_t)n_kv_heads * (rotation == ISOQ_ROT_SO2 ? d : 2 * d));
   isoq_params_generate_v(seed, d, n_kv_heads, rotation, p->host.data());
   cudaError_t e = cudaGetDevice(&p->device);
@@ -392,20 +362,14 @@ int isoq_make_params_v(uint64_t seed, int d, int n_kv_heads, int bits, int rotat
       for (int i = 0; i < 4; ++i) M[i * 4 + j] = (float)z[i];
     }
   }
-  const size_t rot_off = ((nq + mats.size()) * sizeof(float) + 255) / 256 * 256;
-  e = cudaMalloc(&p->dev, rot_off + (size_t)n_kv_heads * d * d * 2 * sizeof(__half));
+  const size_t bytes = (nq + mats.size()) * sizeof(float);
+  e = cudaMalloc(&p->dev, bytes);
   if (e == cudaSuccess) {
     p->dev_mat = p->dev + nq;
-    p->dev_rot = reinterpret_cast<__half*>(reinterpret_cast<char*>(p->dev) + rot_off);
     e = cudaMemcpy(p->dev, p->host.data(), nq * sizeof(float), cudaMemcpyHostToDevice);
   }
   if (e == cudaSuccess)
     e = cudaMemcpy(p->dev_mat, mats.data(), mats.size() * sizeof(float), cudaMemcpyHostToDevice);
-  if (e == cudaSuccess) {
-    rotation_parts_kernel<<<512, 256>>>(p->dev_mat, p->dev_rot, d, n_kv_heads);
-    e = cudaGetLastError();
-    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
-  }
   if (e != cudaSuccess) {
     if (p->dev) cudaFree(p->dev);
     delete p;
@@ -529,7 +493,6 @@ int dequantize_common(const isoq_params* params, const isoq_cache* cache, const 
   if ((rc = check_device(params))) return rc;
   isoq::DequantizeArgs a{};
   a.mats = params->dev_mat;
-  a.rot = params->dev_rot;
   a.bits = params->bits;
   a.n_kv_heads = cache->n_kv_heads;
   a.d = cache->d;

@@ -3,7 +3,7 @@
 //   X[128 vectors x 128 dims] = Z[128 x d] . R  per KV head,  x = (n / sqrt d) (Z R)
 // Z holds the levels of the vectors' codes as binary16 (ALPHA times the level: relative
 // error < 2e-5 at 3 bits, 0 at 2, < 6e-5 at 4), R the head's rotation (WHT and 4x4 blocks
-// in one matrix, made in binary64 with the parameters) as one or two binary16 parts, the
+// in one matrix, made here from the blocks in doubled binary32) as one or two binary16 parts, the
 // sums in the tensor core's binary32.  Rounding: with both parts (fp16 outputs) R keeps 22
 // bits, so the levels' 2e-5 leads, 1/24 of the output's own half step.  bf16 outputs take
 // the high part alone: an entry's relative error of at most 2^-12 to 2^-11 gives elements
@@ -60,7 +60,7 @@ struct ReadSmem {
   static constexpr int kOffNorm = kOffRow + 3 * kTile * (int)sizeof(TileRow);  // float [3][128]
   static constexpr int kOffWhole = kOffNorm + 3 * kTile * 4;  // int [3][8]: 16-row blocks in order
   static constexpr int kOffBar = kOffWhole + 3 * 8 * 4;
-  static constexpr int kOffTmem = kOffBar + 2 * 8;
+  static constexpr int kOffTmem = kOffBar + 8 + 8;
   // the rotary table's 64 pairs of the tile's 64 keys, 512 bytes a row
   static constexpr int kOffTable = (kOffTmem + 16 + 127) / 128 * 128;
   static constexpr int kBytes = ROPE ? kOffTable + 64 * 512 : kOffTmem + 16;
@@ -101,6 +101,22 @@ __device__ __forceinline__ uint32_t pack2(float2 v) {
   }
 }
 
+// (u + v) (a + b + c + d) as x + y to twice binary32's bits, |v| <= ulp(u) / 2: the sums' and the
+// product's rounding errors are kept (Knuth's two-sum, and a fused multiply-add).
+__device__ __forceinline__ float2 scaled_sum(float a, float b, float c, float d, float u, float v) {
+  float s = a, e = 0.f;
+  auto add = [&](float t) {
+    const float r = s + t, w = r - s;
+    e += (s - (r - w)) + (t - w);
+    s = r;
+  };
+  add(b);
+  add(c);
+  add(d);
+  const float p = s * u, err = fmaf(s, u, -p) + fmaf(s, v, e * u), x = p + err;
+  return make_float2(x, (p - x) + err);
+}
+
 // 2 d threads: each takes, of either item (64 rows), one 32-dim group of a row or one group
 // of the V tile layout.
 template <int D, int BITS, typename T, bool LO, bool ROPE>
@@ -117,7 +133,7 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
   TileRow* rows = reinterpret_cast<TileRow*>(smem + SM::kOffRow);  // [3 tiles][128]
   float* nrm = reinterpret_cast<float*>(smem + SM::kOffNorm);
   int* whole = reinterpret_cast<int*>(smem + SM::kOffWhole);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);  // R loaded, products done
+  uint64_t* done = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);  // the products
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kOffTmem);
   const uint32_t sB = smem_u32(smem), sA = smem_u32(smem + SM::kOffA);
 
@@ -270,15 +286,32 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
   // ---- R into shared memory, tensor memory, the first tiles' rows and words -------------
   if (warp == 0) tc::alloc(tmem_slot, kTileCols);
   if (tid == 0) {
-    mbar_init(bars, 1);
-    mbar_init(bars + 1, 1);
+    mbar_init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    const uint8_t* src = static_cast<const uint8_t*>(a.rot) + (size_t)unit * 2 * SM::kPart;
-    mbar_expect_tx(bars, SM::kOffA);
-    for (int o = 0; o < SM::kOffA; o += 32768) bulk_copy(smem + o, src + o, 32768, bars);
   }
+  // Column n of R is (-1)^popc(k & dim) times one of four sums of block k / 4's row, by dim % 4 (the
+  // Sylvester matrix's rows 4 kb + j, j = 0..3): 4 d values in all, two a thread.  They go to the
+  // operand tile's place, [k / 8][dim % 4][k % 8], the second part behind the first.
+  static_assert(4 * D == 2 * NT, "two values a thread");
+  const float4* mat = reinterpret_cast<const float4*>(a.mats + (size_t)h * D * 4);
+  float4 m[2];  // row x % 4 of block x / 16, x = tid, tid + NT
+#pragma unroll
+  for (int y = 0; y < 2; ++y) m[y] = __ldg(mat + ((tid + y * NT) >> 4) * 4 + (tid & 3));
   fetch_token(first);
   fetch_page();
+  constexpr double kUnit = kRotScale / (D == 256 ? 16.0 : 11.313708498984761);  // / sqrt(d)
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int kb = (tid + y * NT) >> 4, row = tid & 3, odd = (tid >> 2) & 3;
+    const float2 r = scaled_sum(m[y].x, (odd & 1) ? -m[y].y : m[y].y, (odd & 2) ? -m[y].z : m[y].z,
+                                (odd == 1 || odd == 2) ? -m[y].w : m[y].w, (float)kUnit,
+                                (float)(kUnit - (double)(float)kUnit));
+    const int at = (kb >> 1) * 32 + odd * 8 + (kb & 1) * 4 + row;
+    if (!in_bounds(at < 4 * D, a.status)) continue;
+    __half* t = reinterpret_cast<__half*>(smem + SM::kOffA) + at;
+    t[0] = __float2half_rn(r.x);
+    if constexpr (LO) t[4 * D] = __float2half_rn((r.x - __half2float(t[0])) + r.y);
+  }
   fetch_token(first + step);
   put_row(0);
   fetch_page();
@@ -289,6 +322,21 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
   const uint32_t tmem = __shfl_sync(kFull, *tmem_slot, 0);
   const int role = __shfl_sync(kFull, warp, 0);  // warp-uniform to the compiler as well
   load_words(0);
+  {
+    const int n = tid & 127, dim = read_column(D, q, n);  // R in the no-swizzle K-major layout:
+#pragma unroll
+    for (int k8 = tid >> 7; k8 < D / 8; k8 += NT / 128) {  // 16 bytes of k = 8 k8 .. + 7, column n
+      const uint32_t s0 = (__popc(8 * k8 & dim) & 1) ? 0x80008000u : 0u;
+      const uint32_t s1 = (__popc((8 * k8 + 4) & dim) & 1) ? 0x80008000u : 0u;
+#pragma unroll
+      for (int part = 0; part < (LO ? 2 : 1); ++part) {
+        const uint4 v = *reinterpret_cast<const uint4*>(smem + SM::kOffA + part * 8 * D + k8 * 64 + (dim & 3) * 16);
+        if (in_bounds(part * SM::kPart + k8 * 2048 + n * 16 + 16 <= SM::kOffA, a.status))
+          st_chunk(sB + part * SM::kPart + k8 * 2048 + n * 16, v.x ^ s0, v.y ^ s0, v.z ^ s1, v.w ^ s1);
+      }
+    }
+  }
+  __syncthreads();  // the sums have been read: the operand tile takes their place
 
   const int row0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);  // tensor-memory lanes row0 ..
   const uint32_t t_rows = tmem + ((uint32_t)row0 << 16);
@@ -312,8 +360,7 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
     put_row(st1);
     fence_proxy_async();  // the tile's generic-proxy writes, before the tensor core reads them
     tc::fence_before();
-    if (k == 0) ok = mbar_wait(bars, 0);
-    if (__syncthreads_or(!ok)) {  // the tile's only barrier
+    if (__syncthreads_or(!ok)) {  // the tile's only barrier without a rotary table
       fail = true;
       break;
     }
@@ -326,7 +373,7 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
           tc::mma_ss(tmem, ad + kk * 256, bd + kk * 256, kId, kk > 0);
           if constexpr (LO) tc::mma_ss(tmem, ad + kk * 256, bd + SM::kPart / 16 + kk * 256, kId, 1);
         }
-        tc::commit(bars + 1);
+        tc::commit(done);
       }
       __syncwarp();
     }
@@ -347,7 +394,7 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
     fetch_token(tile + 3ll * step);
 
     // ---- the product's rows: scale, rotary embedding, round, out --------------------------
-    ok = __all_sync(kFull, mbar_wait(bars + 1, k & 1));  // warp-uniform: collective loads
+    ok = __all_sync(kFull, mbar_wait(done, k & 1));  // warp-uniform: collective loads
     if constexpr (ROPE) {
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();
@@ -395,10 +442,7 @@ __global__ void __launch_bounds__(2 * D, read_ctas<D, LO>(ROPE))
   if (__syncthreads_or(!ok) || fail) {
     // a bounded wait gave up: wait (bounded) for what is in flight, then release
     if (tid == 0) set_status(a.status, ISOQ_ST_TIMEOUT);
-    mbar_wait(bars, 0);
-    if (pending) mbar_wait(bars + 1, (k - 1) & 1);
-  } else if (first >= n_tiles) {
-    mbar_wait(bars, 0);  // no tile: R's copy must have landed before the CTA ends
+    if (pending) mbar_wait(done, (k - 1) & 1);
   }
   tc::fence_before();
   __syncthreads();
@@ -445,10 +489,11 @@ cudaError_t launch_tc_t(const DequantizeArgs& a, cudaStream_t stream, int n_sm) 
 
 }  // namespace
 
-// From 2^20 elements on (8192 vectors of 128, 4096 of 256): below, loading R and the chain of
-// one tile cost more than the warp kernel's shuffles.  Measured, bf16, 8 KV heads, d = 128 /
-// 256, us a call (this kernel | the warp kernel): 256 tokens 4.8 | 3.8 / 5.7 | 6.0, 512 tokens
-// 4.9 | 5.2 / 5.9 | 10.7, 4096 tokens 9.0 | 18 / 22 | 33.  fp16 with the rotary embedding at d =
+// From 2^20 elements on (8192 vectors of 128, 4096 of 256): below, making R and the chain of
+// one tile cost more than the warp kernel's shuffles.  Measured, 8 KV heads, d = 128 / 256, us a
+// call (this kernel | the warp kernel), bf16: 256 tokens 5.1 | 3.7 / 6.4 | 6.0, 512 tokens
+// 5.1 | 5.0 / 6.6 | 10.4, 4096 tokens 9.8 | 17.5 / 22.0 | 32.9; fp16: 512 tokens 5.7 | 5.1 /
+// 7.5 | 10.4, 1024 tokens 5.8 | 8.0 / 10.5 | 18.8.  fp16 with the rotary embedding at d =
 // 256 stays with the warp kernel: both parts of R leave no room for the staged table, and
 // reading it in place took 330 us for 32768 tokens against 280.
 bool use_dequantize_tc(const DequantizeArgs& a) {

@@ -44,7 +44,6 @@ struct QuantizeArgs {
 // Read-back of listed tokens; by value to the kernels.
 struct DequantizeArgs {
   const float* mats;    // device [H][d/4][4][4]: block rotations as matrices
-  const void* rot;      // device: the inverse rotation's binary16 operands (isoq_api.cu)
   int bits, n_kv_heads, d;
   const uint8_t* blocks;
   const int32_t* page_table;
