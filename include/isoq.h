@@ -425,9 +425,9 @@ int isoq_multi_token_attention(const isoq_params* params, const isoq_cache* cach
  *
  * window >= 1, n_sinks >= 0.  max_seq_len: a host upper bound of seq_lens, the one given
  * to isoq_window_workspace_bytes; a longer seq_lens[s] is clamped to it (and to the page
- * table) with ISOQ_ST_LEN_RANGE, a negative one is 0.  Q, out: device, 16-byte aligned;
- * out has the shape of Q and the element type out_dtype (ISOQ_F32, ISOQ_BF16, ISOQ_F16; the result in binary32 is rounded once,
- * to nearest).  workspace: device, 16-byte aligned, at least
+ * table, and to 2^31 - 64) with ISOQ_ST_LEN_RANGE, a negative one is 0.  Q, out: device,
+ * 16-byte aligned; out has the shape of Q and the element type out_dtype (ISOQ_F32, ISOQ_BF16,
+ * ISOQ_F16; the result in binary32 is rounded once, to nearest).  workspace: device, 16-byte aligned, at least
  * isoq_window_workspace_bytes(...) bytes (n_q = 1 for the decode); contents need not be
  * initialised; calls that share a workspace must not overlap.
  * isoq_window_workspace_bytes returns 0 for sizes that the calls refuse.

@@ -72,12 +72,14 @@ __device__ __forceinline__ bool win_sees(const WinArgs& w, int lo, int t) {
 }
 
 // A sequence's length as the kernels use it: clamped to the page table, and with a window
-// to the bound that the split plan was made for (either sets ISOQ_ST_LEN_RANGE).
+// to the bound that the split plan was made for and to 2^31 - 64, up to which the positions of
+// its last page and the one behind it are ints (each sets ISOQ_ST_LEN_RANGE).
 template <bool WIN>
 __device__ __forceinline__ int clamp_len(int len, int max_pages, const WinArgs& w, bool report,
                                          uint32_t* status) {
   int most = max_pages * kPage;
-  if constexpr (WIN) most = (int)min((long long)w.max_len, (long long)max_pages * kPage);
+  if constexpr (WIN)
+    most = (int)min((long long)min(w.max_len, 0x7FFFFFFF - (kPage - 1)), (long long)max_pages * kPage);
   if (len > most) {
     if (report) set_status(status, ISOQ_ST_LEN_RANGE);
     len = most;

@@ -84,3 +84,46 @@ def test_a_workspace_of_the_size_asked_for_is_enough(oracle, kw):
     with pytest.raises(iq.IsoqError) as e:
         c.run(ws=raw[:n - 1])
     assert e.value.code == iq.ISOQ_E_WORKSPACE
+
+
+@pytest.mark.parametrize("d,bits,n_q", [(128, 3, 1), (128, 3, 3), (128, 3, 40), (128, 4, 2), (256, 3, 1)])
+def test_lengths_next_to_the_largest_position(oracle, d, bits, n_q):
+    """Tokens just below 2^31: a length up to 2^31 - 64 is attended as any other, a longer one is
+    clamped to that and reported."""
+    end, maxp, H, keep = 2 ** 31 - 64, 2 ** 25, 2, 200
+    params = iq.isoq_make_params(80, d, H, bits=bits)
+    cache = iq.PagedCache(d, H, 8, torch.full((1, maxp), -1, dtype=torch.int32), bits=bits)
+    first = (end - keep) // 64
+    cache.page_table[0, first:first + 5] = torch.arange(5, dtype=torch.int32, device="cuda").flip(0)
+    g = torch.Generator().manual_seed(5)
+    pos = torch.arange(end - keep, end + 60, dtype=torch.int64).to(torch.int32)
+    K, V = torch.randn((2, len(pos), H, d), generator=g)
+    V[keep:] *= 1e3                        # behind the last position that can be attended
+    iq.isoq_quantize_append(params, cache, K.cuda(), V.cuda(), torch.zeros(len(pos), dtype=torch.int32, device="cuda"),
+                            pos.cuda())
+    Q = torch.randn((1, n_q, 8, d), generator=g).cuda()
+    W, L = 100, 2 ** 31 - 1
+    ws = torch.empty(max(16, iq.isoq_window_workspace_bytes(1, n_q, 8, H, d, L, W, 0)), dtype=torch.uint8, device="cuda")
+
+    def run(n):
+        out = torch.full_like(Q, float("nan"))
+        iq.isoq_multi_token_attention_window(params, cache, Q, torch.tensor([n], dtype=torch.int32, device="cuda"), L,
+                                             W, 0, out, d ** -0.5, ws)
+        return out
+    want = run(end)
+    assert iq.isoq_get_status(cache) == 0
+    # the same tokens in a short cache
+    short = iq.PagedCache(d, H, 8, torch.arange(5, dtype=torch.int32).flip(0)[None], bits=bits)
+    short.blocks.copy_(cache.blocks)
+    n = end - first * 64
+    other = torch.full_like(Q, float("nan"))
+    iq.isoq_multi_token_attention_window(params, short, Q, torch.tensor([n], dtype=torch.int32, device="cuda"), n, W, 0,
+                                         other, d ** -0.5, ws if ws.numel() > 1 << 20 else
+                                         torch.empty(1 << 22, dtype=torch.uint8, device="cuda"))
+    assert bool(torch.isfinite(want).all()) and bool(want.any())
+    assert float((want - other).norm() / other.norm()) <= 2 * 5e-4  # each within 5e-4 of the definition
+    for n in (end + 1, end + 60, L):
+        got = run(n)
+        assert iq.isoq_get_status(cache) == iq.ISOQ_ST_LEN_RANGE, n
+        iq.isoq_reset_status(cache)
+        assert torch.equal(got, want), n
