@@ -5,6 +5,7 @@ The refusal is made on the host: work on a stream whose capture has been invalid
 synchronisation, which a capturing stream does not allow) is turned down before anything is
 launched."""
 import ctypes
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -52,6 +53,12 @@ def _calls(c):
 
 @pytest.mark.parametrize("bits", [3, 4])
 def test_a_refused_launch_leaves_no_error_behind(bits):
+    # in a thread of its own: isoq_last_cuda_error, which is the thread's, is left set
+    with ThreadPoolExecutor(1) as pool:
+        pool.submit(_refuse_each, bits).result()
+
+
+def _refuse_each(bits):
     c = Case([300], 8, 2, 100, 4, n_q=40, bits=bits, seed=3, poison=False)
     calls, keep = _calls(c)
     rt = ctypes.CDLL("libcudart.so.12")  # the runtime that the library and torch share
