@@ -283,9 +283,10 @@ int isoq_quantize_append_layers(const isoq_params* const* params,
  * slot that was never appended reads as whatever its bytes stand for.  rope_table: device,
  * 16-byte aligned, as for isoq_quantize_append_rope.  n_tokens == 0 is a no-op.
  * Arithmetic: sums in binary32.  To fp32, and for short lists, the levels and the rotation are
- * binary32 as well; from 2^20 elements on, 16-bit outputs take the levels as binary16 (relative
- * error < 6e-5) and the rotation as binary16, in two parts for fp16 (22 bits), in one for bf16
- * (11 bits: ~1.5e-4 of the vector's rms, a tenth of what rounding to bf16 costs).
+ * binary32 as well; from 2^20 elements on (of K and V together), 16-bit outputs take the levels
+ * as binary16 (relative error < 6e-5) and the rotation as binary16, in two parts for fp16 (22
+ * bits), in one for bf16 (11 bits: ~1.5e-4 of the vector's rms, a tenth of what rounding to bf16
+ * costs); fp16 at d = 256 with a rope_table stays with binary32.
  * Errors: ISOQ_E_ARG, ISOQ_E_DIM, ISOQ_E_DEVICE, ISOQ_E_CUDA.
  * ===================================================================================== */
 int isoq_dequantize(const isoq_params* params, const isoq_cache* cache, const int32_t* seq_ids,

@@ -110,14 +110,14 @@ struct SplitPlan {
 #define ISOQ_MQ_WAVES 8
 #endif
 
-// Context chunking for the decode kernel: about ISOQ_DEC_WAVES waves of (chunk, KV head,
-// query-head block, sequence) CTAs at the kernel's resident CTAs per SM, each chunk a whole
-// number of pages and at least min_pages pages when the context allows.
 // Pages of a context of at most len tokens (at least one, so that a plan has a chunk).
 int pages_of(int len) {
   return len > 0 ? (int)(((long long)len + ISOQ_PAGE_SIZE - 1) / ISOQ_PAGE_SIZE) : 1;
 }
 
+// Context chunking for the decode kernel: about ISOQ_DEC_WAVES waves of (chunk, KV head,
+// query-head block, sequence) CTAs at the kernel's resident CTAs per SM, each chunk a whole
+// number of pages and at least min_pages pages when the context allows.
 SplitPlan plan_splits(int n_seqs, int n_q_heads, int n_kv_heads, int d, int max_seq_len,
                       int n_q = 1) {
   const int group = n_kv_heads > 0 ? n_q_heads / n_kv_heads : 1;

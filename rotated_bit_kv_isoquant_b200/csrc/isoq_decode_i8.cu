@@ -159,7 +159,8 @@ struct I8Smem {
   static constexpr int kKfOff = kA2Off + (D / 32) * 32 * 16;           // float [8]
   static constexpr int kRowOff = kKfOff + 8 * 4;                      // int [8]
   static constexpr int kBytes = kRowOff + 8 * 4;
-  // the warps' states [NW][8][D + 4] and, for a single chunk, the merged rows [8][D + 1]
+  // the warps' states [NW][8][D + 4] and the merged rows: [8][D + 4] of a windowed call
+  // (finish_stride), [8][D + 1] of a whole-context one with a single chunk
   static constexpr int kMergeBytes = NW * 8 * (D + 4) * 4 + 8 * (D + 4) * 4;
   static_assert(kMergeBytes <= kRing, "merge buffer must fit in the ring");
   static_assert(kAOff % 16 == 0 && kA2Off % 16 == 0, "A fragments must be aligned");

@@ -169,7 +169,11 @@ cudaError_t launch_clustered(void (*kernel)(P...), dim3 grid, int threads, size_
 }
 
 // Windowed chunks with more than 32 rows per KV head (d = 128) take the tensor-memory kernel,
-// 128 rows a CTA or 256 where a KV head has more; the others the row-block kernels.
+// 128 rows a CTA or 256 where a KV head has more; the others the row-block kernels.  Measured, 8
+// KV heads, us (row blocks | tensor memory) at 24, 32 and 40 rows: 3 bits, 16 sequences, window
+// 4096 75 | 89, 94 | 89, 130 | 89; 64 sequences, window 1024 103 | 131, 134 | 132, 166 | 132; one
+// sequence, window 4096 16 | 21, 18 | 21, 19 | 22.  2 and 4 bits follow the same rule although
+// the 4-bit row blocks lose earlier: 16 sequences 108 | 94, 144 | 95, 199 | 95.
 inline bool use_window_tc(int d, int n_q, int group) {
   return d == 128 && n_q > 1 && (long long)n_q * group > 32;
 }

@@ -71,7 +71,8 @@ struct WinSmem {
   static constexpr int kBB = block_bytes(kWD, BITS);
   // at 0: the queries, [2 halves][hi, lo], at the end the halves' merge
   // (k-groups 2048 + 16 bytes apart, so that a row's 8-byte stores spread over the banks)
-  static constexpr int kQGroup = 2064, kQPart = 16 * kQGroup + 240;  // a multiple of 256
+  static constexpr int kQGroup = 2064, kQPart = 16 * kQGroup;
+  static_assert(kQPart % 256 == 0, "the tiles behind the queries start on 256 bytes");
   static constexpr int kOffK = 4 * kQPart;              // [2] K_hat tiles
   static constexpr int kOffV = kOffK + 2 * kPageTile;   // [2] V_hat tiles
   static constexpr int kOffRing = kOffV + 2 * kPageTile;
