@@ -41,7 +41,7 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[E]) {
 // dims l E .. l E + E-1 and the head's blocks of them.  The run's pages are looked up at once, a
 // token a lane, and the next token's words are loaded while one is computed.  The shuffles of
 // the WHT bound it (20 a vector at d = 128, with the loads ~30 of the load-store pipe's cycles):
-// 32768 tokens x 8 heads to fp32 in 111 us (2.7 TB/s), at d = 256 in 199 (3.0 TB/s); 188 with a
+// 32768 tokens x 8 heads to fp32 in 107 us (2.8 TB/s), at d = 256 in 208 (2.8 TB/s); 188 with a
 // token a warp, which the lookups bounded, 158 with four heads of a token a warp, whose blocks
 // were loaded again for each.
 constexpr int kDqWarps = 8;

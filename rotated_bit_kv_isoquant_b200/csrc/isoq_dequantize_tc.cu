@@ -20,11 +20,13 @@
 // reads the V tile layout's groups as they are, four tokens at a time; other tokens pick
 // their own nibbles out of the groups.
 //
-// Measured (32768 consecutive tokens, 8 KV heads, K and V): d = 128 to bf16 45 us (3.6 TB/s of
-// codes read and values written), to fp16 53 us, with the rotary embedding 74 and 109 us;
-// d = 256 to bf16 139 us, with the embedding 234.  ncu on the first: ALU pipe 57% busy, issue
-// 56% of the cycles, DRAM 28%, tensor pipe 20%: bound by the instructions of the fill and the
-// write-out (44 a vector) and by the chain of one tile's steps.  Tried, the first in us: the
+// Measured (32768 consecutive tokens, 8 KV heads, K and V): d = 128 to bf16 47 us (3.4 TB/s of
+// codes read and values written), to fp16 53 us, with the rotary embedding 72 and 107 us;
+// d = 256 to bf16 134 us, with the embedding 231.  ncu on the first: ALU pipe 55% busy, issue
+// 55% of the cycles, DRAM 27%, tensor pipe 20%: bound by the instructions of the fill and the
+// write-out (44 a vector) and by the chain of one tile's steps.  R made by every CTA (~0.3 us)
+// instead of read from a copy kept with the parameters: bf16 1.4 us longer, the others 0.6 to 7
+// shorter.  Tried, with 45 us for the first: the
 // output staged in shared memory and sent as one bulk copy a row, 57-70 (the copy engine takes
 // ~33 cycles a row), or written by 16 lanes a row, 57; each thread writing its own row's
 // columns, 56 (32 lines an instruction); the page lookups not pipelined, 70; twice the threads

@@ -25,10 +25,11 @@
 // A call whose rows' pages fit one chunk divides, rotates back and writes its output here.
 // Otherwise partial states go to the combine.
 //
-// Measured (64 query / 8 KV heads, window 4096): 2048 query tokens of one sequence 532 us (517
-// TFLOP/s of scores and values, the low query part not counted), 16 tokens of 8 sequences 70 us.
-// A page of 256 rows takes ~3800 cycles, of which a softmax warp computes ~2500: its latency
-// bounds the kernel (issue 49% of the cycles, tensor pipe 37%, exponent unit 26%).  Why this
+// Measured (64 query / 8 KV heads, window 4096): 2048 query tokens of one sequence 540 us (509
+// TFLOP/s of scores and values, the low query part not counted), 574 where most norms are a
+// twentieth of the first ones and rows are lifted; 16 tokens of 8 sequences 71 us.
+// A page of 256 rows takes ~3900 cycles, of which a softmax warp computes ~2500: its latency
+// bounds the kernel (issue 48% of the cycles, tensor pipe 35%, exponent unit 25%).  Why this
 // split: one CTA of 128 threads doing the steps in turn, two per SM, took 1266 us; the score
 // products read A and B from shared memory (48 cycles of its bandwidth for 32 of the tensor
 // core), so 256 rows share a page's tiles, and the next page's scores are issued before this
