@@ -72,3 +72,30 @@ def test_rows_whose_first_values_are_zero(oracle, i):
     c = Case(lens, W=140, S=3, out="f32", q="f32", seed=60 + i, poison=False, **f)
     _with_norms(c, lambda s, p: 3e4 if p == lens[s] - 1 else 0.0 if p < lens[s] - 110 else 0.01)
     c.check(oracle, c.run())
+
+
+@pytest.mark.parametrize("where", ["ahead", "behind", "middle"])
+@pytest.mark.parametrize("f", [dict(n_q=3, hq=8, hkv=2), dict(n_q=10, hq=8, hkv=2), dict(n_q=70, hq=8, hkv=2),
+                               dict(n_q=3, hq=4, hkv=1, bits=4), dict(n_q=2, hq=4, hkv=1, d=256)])
+def test_large_values_with_the_window_in_several_chunks(oracle, f, where):
+    """The chunks' states meet in the workspace or in a cluster: the rows of each chunk keep
+    references of their own."""
+    lens, W, n_q = [9000], 8000, f["n_q"]
+    c = Case(lens, W=W, S=2, out="f32", q="f32", seed=90, poison=False, **f)
+    big = {"ahead": [lens[0] - 1], "behind": [lens[0] - n_q - W + 1], "middle": list(range(4000, 4100))}[where]
+    _with_norms(c, lambda s, p: 3e4 if p in big else 3e-3)
+    c.check(oracle, c.run())
+
+
+def test_lifted_rows_repeat_bitwise_and_in_a_graph():
+    c = Case([400, 193], 8, 2, 90, 0, n_q=64, out="f32", q="f32", seed=5, poison=False)
+    _with_norms(c, lambda s, p: 3e4 if p in (399, 192) else 3e-3)
+    want, out, ws = c.run(), torch.empty_like(c.run()), c.workspace()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(ws=ws, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+    assert iq.isoq_get_status(c.cache) == 0

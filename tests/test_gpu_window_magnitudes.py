@@ -64,3 +64,24 @@ def test_zero_queries_and_fp16_ones_near_their_largest(oracle, i):
     Q[:, :, ::3] = 0
     scale = c.d ** -0.5 * 2.0 ** -16
     check(c, oracle, Q, scale, run(c, Q, scale))
+
+
+@pytest.mark.parametrize("k", [-30, 14])
+@pytest.mark.parametrize("f", [dict(n_q=3), dict(n_q=12), dict(n_q=50), dict(n_q=1, bits=4), dict(n_q=3, bits=2)])
+def test_queries_with_the_window_in_several_chunks(oracle, f, k):
+    c = Case([9000], 8, 2, 8000, 4, q="f32", out="f32", seed=70, **f)
+    Q, scale = c.Q * 2.0 ** k, c.d ** -0.5 * 2.0 ** -k
+    check(c, oracle, Q, scale, run(c, Q, scale))
+
+
+def test_a_row_that_is_not_finite_stays_alone():
+    """NaN and infinite queries give rows that are not finite; every other row keeps its bits."""
+    for n_q, bits in ((1, 3), (3, 3), (40, 3), (100, 3), (3, 4), (40, 4)):
+        c = Case([300, 190], 8, 2, 150, 4, n_q=n_q, bits=bits, q="f32", out="f32", seed=80, poison=False)
+        want = run(c, c.Q, c.d ** -0.5)
+        Q = c.Q.clone()
+        Q[0, n_q // 2, 3, 5], Q[1, 0, 7, 100] = float("nan"), float("inf")
+        got = run(c, Q, c.d ** -0.5)
+        bad = torch.zeros(Q.shape[:-1], dtype=torch.bool)
+        bad[0, n_q // 2, 3] = bad[1, 0, 7] = True
+        assert torch.equal(got[~bad.cuda()], want[~bad.cuda()]), (n_q, bits)
