@@ -421,14 +421,16 @@ int isoq_multi_token_attention(const isoq_params* params, const isoq_cache* cach
  * codes, any norms, infinities and NaN included): a caller may recycle a page for another
  * sequence as soon as the window has passed its last token.
  *
- * Q's elements may be of any size up to 2^100 with a scale to match: a query is scaled by a power
- * of two of its own where binary16 operands would not hold it.
+ * A query may be of any size (its largest element between 2^-80 and 2^100, or zero) with a
+ * scale to match: it is scaled by a power of two of its own where binary16 operands would not
+ * hold it.
  *
  * window >= 1, n_sinks >= 0.  max_seq_len: a host upper bound of seq_lens, the one given
  * to isoq_window_workspace_bytes; a longer seq_lens[s] is clamped to it (and to the page
  * table, and to 2^31 - 64) with ISOQ_ST_LEN_RANGE, a negative one is 0.  Q, out: device,
  * 16-byte aligned; out has the shape of Q and the element type out_dtype (ISOQ_F32, ISOQ_BF16,
- * ISOQ_F16; the result in binary32 is rounded once, to nearest).  workspace: device, 16-byte aligned, at least
+ * ISOQ_F16; the result in binary32 is rounded once, to nearest).  workspace: device, 16-byte
+ * aligned, at least
  * isoq_window_workspace_bytes(...) bytes (n_q = 1 for the decode); contents need not be
  * initialised; calls that share a workspace must not overlap.
  * isoq_window_workspace_bytes returns 0 for sizes that the calls refuse.

@@ -59,6 +59,25 @@ __device__ __forceinline__ constexpr uint32_t col_s(int w) { return 64 * w; }
 __device__ __forceinline__ constexpr uint32_t col_p(int w) { return 128 + 32 * w; }
 __device__ __forceinline__ constexpr uint32_t col_o(int w) { return 256 + 128 * w; }
 
+// The weights p |v| / sigma go to the value product as binary16, whose subnormals below 2^-14 cost
+// them bits, and sigma is the largest |v| of the tokens that any row of the CTA sees.  For a row
+// that sees much smaller ones the reference is sigma / 2^bits instead, near the row's own largest,
+// by keeping p 2^bits for p: its running maximum is `bits` lower, sums and outputs divide by it.
+// Weights reach 2^(kLazy + kLift) kSigmaSlack = 2^15 at most, and a subnormal's half step is at
+// most 2^-25 of the row's largest |v| times its largest p: kLift pays for norms down to sigma / 8,
+// which need no lift.
+constexpr float kLift = 3.f;
+constexpr float kSpreadNorms = 8.f;  // 2^kLift
+// The bits for a tile or page whose tokens that the row sees have norms of at most v (0: none);
+// `bits` as before, if it still does.
+__device__ __forceinline__ float lift_bits(float v, float sigma, float bits) {
+  const float ref = sigma * ex2(-bits);
+  if (v > 0.f && ref <= kSpreadNorms * v && v <= kSigmaSlack * ref) return bits;
+  // a power of two above sigma / v, by the exponents
+  const int over = (int)(__float_as_uint(sigma) >> 23) - (int)(__float_as_uint(v) >> 23) + 1;
+  return v > 0.f && sigma > kSpreadNorms * v ? (float)over : 0.f;
+}
+
 // A page as the softmax takes it: it has data; some row may need a lift on it (lift_bits: a token
 // that some row sees has |v| < sigma / kSpreadNorms); none does, but on the half's page before.
 enum PageState { kValid = 1, kSpread = 2, kLevel = 4 };

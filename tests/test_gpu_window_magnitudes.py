@@ -39,7 +39,7 @@ def check(c, oracle, Q, scale, got):
     assert iq.isoq_get_status(c.cache) == 0
 
 
-@pytest.mark.parametrize("k", [-60, -30, -14, -8, 8, 11, 14, 30, 60])
+@pytest.mark.parametrize("k", [-80, -60, -30, -14, -8, 8, 11, 14, 30, 60, 94])
 @pytest.mark.parametrize("i", range(len(FORMS)))
 def test_a_query_and_its_scale_by_powers_of_two(oracle, i, k):
     c = Case([300, 190], 12, 3, 150, 4, q="bf16" if i % 2 else "f32", out="f32", seed=i, **FORMS[i])
